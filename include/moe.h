@@ -290,6 +290,115 @@ MOE_API moe_status moe_layer_graph_create(const moe_config *cfg, const moe_weigh
 MOE_API moe_status moe_layer_graph_launch(moe_layer_graph graph, cudaStream_t stream);
 MOE_API moe_status moe_layer_graph_destroy(moe_layer_graph graph);
 
+/* ------------------------------------------------------------------------------------
+ * Norms around a block, fused with its gate and residual scale
+ * ------------------------------------------------------------------------------------
+ * How a block's gate multiplies its branch: not at all, one value per channel [d], one
+ * per token [T], or one per element [T, d]. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate;
+
+/* Sizes and types of a block norm over T tokens (at most 2^30) x d_model channels (a
+ * multiple of 8, at most 16384).
+ *   res     r, r_out, dr_out, dr (the residual stream)    MOE_BF16 or MOE_F32
+ *   act     y, dy, dh and a MOE_GATE_FULL gate / dgate    MOE_BF16 or MOE_F32
+ *   weight  w_post, w_pre, a channel or token gate        MOE_BF16 or MOE_F32
+ *   out     h: MOE_BF16, MOE_F32, or MOE_E4M3 (d_model % 128 == 0): codes with one
+ *           power-of-two fp32 scale per 128 channels, by the rule of moe_permute -- the form
+ *           moe_layer_forward takes as MOE_E4M3 activations and moe_grouped_gemm as rows
+ *   eps > 0; res_scale and branch_scale finite; w_offset is added to both norm weights (1 for
+ *   weights stored as differences from one, else 0) */
+typedef struct {
+  int32_t T, d_model;
+  moe_gate gate;
+  moe_dtype res, act, weight, out;
+  float eps, res_scale, branch_scale, w_offset;
+} moe_norm_config;
+
+/* Bytes of workspace moe_block_norm_backward needs.  Host only; no CUDA call. */
+MOE_API moe_status moe_norm_workspace_size(const moe_norm_config *cfg, size_t *bytes);
+
+/* The end of one block and the start of the next:
+ *   u     = norm(y; w_post)                      (u = y when w_post is NULL)
+ *   r_out = res_scale * r + branch_scale * gate * u
+ *   h     = norm(r_out; w_pre)
+ *   norm(x; w) = x / sqrt(mean(x^2) + eps) * (w + w_offset)   per token
+ * in fp32 registers, each output rounded once (h from the unrounded r_out).
+ *   y      NULL: no branch (r_out = res_scale * r; gate and w_post NULL, gate kind NONE)
+ *   w_pre  NULL: no second norm (h NULL)
+ *   r_out  NULL: not stored
+ *   h_scale [T, d/128] fp32 when cfg->out is MOE_E4M3, else NULL
+ * r_out may be r itself; h may be y or r itself where the types have one size.  Tensors
+ * 16-byte aligned (a token gate and h_scale: by their element). */
+MOE_API moe_status moe_block_norm(const moe_norm_config *cfg, const void *r, const void *y,
+                                  const void *w_post, const void *gate, const void *w_pre, void *r_out,
+                                  void *h, float *h_scale, cudaStream_t stream);
+
+/* Gradients of moe_block_norm.  r_out, y, w_post, gate, w_pre as in the forward call (the
+ * norms' statistics are recomputed from r_out and y); dh [T, d] (cfg->act; required with
+ * w_pre) and dr_out [T, d] (cfg->res; NULL = 0) are the gradients of h and r_out.  With
+ *   G    = dr_out + dnorm(r_out; w_pre)^T dh
+ *   dr   = res_scale * G                              [T, d] cfg->res
+ *   dy   = dnorm(y; w_post)^T (branch_scale gate G)   [T, d] cfg->act (required with y)
+ *   dgate = branch_scale G u, summed to the gate's shape: fp32 [d] or [T], or cfg->act [T, d]
+ *   dw_post, dw_pre [d] fp32
+ * dgate, dw_post and dw_pre may be NULL (not computed).  Sums over tokens run in a fixed
+ * order (bit-identical reruns); T = 0 writes zeros to the [d] gradients.  cfg->out is not
+ * used.  dr may be dr_out and dy may be dh or y where the types match.  Of the workspace
+ * only what lies behind its first 256 bytes is used; it need not be zeroed. */
+MOE_API moe_status moe_block_norm_backward(const moe_norm_config *cfg, const void *r_out, const void *y,
+                                           const void *w_post, const void *gate, const void *w_pre,
+                                           const void *dh, const void *dr_out, void *dr, void *dy,
+                                           void *dgate, float *dw_post, float *dw_pre, void *ws,
+                                           size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Products grouped by expert, one at a time
+ * ------------------------------------------------------------------------------------
+ * n_groups weight matrices [n, k] and up to n_rows rows sorted into groups (as moe_permute
+ * leaves them): group g holds rows group_offsets[g] .. group_offsets[g + 1] - 1.
+ *   in   MOE_BF16 (n and k multiples of 8) or MOE_E4M3_FP32_SCALE (n % 8 == 0, k % 16 == 0;
+ *        moe_grouped_gemm only)
+ *   out  MOE_BF16 or MOE_F32
+ * 1 <= n_groups <= 1024; n, k <= 65536. */
+typedef struct {
+  int32_t n_groups, n_rows, n, k;
+  moe_dtype in, out;
+} moe_product_config;
+
+/* Bytes of workspace the grouped products need.  Host only; no CUDA call. */
+MOE_API moe_status moe_product_workspace_size(const moe_product_config *cfg, size_t *bytes);
+
+/* y[r] = a[r] W_g^T for the rows r of group g.
+ *   group_offsets [n_groups + 1] int32 DEVICE, non-decreasing, <= n_rows; NULL with one group:
+ *                 all n_rows rows.  Offsets that decrease, are negative or pass n_rows set the
+ *                 device status MOE_ERR_DEVICE_INDEX and nothing is computed.
+ *   a [n_rows, k], w [n_groups, n, k], y [n_rows, n] (cfg->out); rows outside the groups are
+ *                 neither used nor written
+ *   a_scale, w_scale  MOE_E4M3_FP32_SCALE: fp32 [n_rows, ceil(k/128)] and
+ *                 [n_groups, ceil(n/128), ceil(k/128)], one scale per 128 codes of a row and per
+ *                 128 x 128 codes of a weight, of any finite value; else NULL.  The product of
+ *                 each 128-k block is summed on the tensor cores and multiplied by its two
+ *                 scales in fp32.
+ * A dense 8-bit product is this call with one group.  a, w, y 16-byte aligned.  The first 256
+ * bytes of the workspace hold the device status (moe_reset_device_status once before use). */
+MOE_API moe_status moe_grouped_gemm(const moe_product_config *cfg, const int32_t *group_offsets,
+                                    const void *a, const float *a_scale, const void *w,
+                                    const float *w_scale, void *y, void *ws, size_t ws_bytes,
+                                    cudaStream_t stream);
+
+/* The gradient of the rows, da[r] = dy[r] W_g: dy [n_rows, n] bf16, w [n_groups, n, k] bf16,
+ * da [n_rows, k] (cfg->out).  Offsets, rows outside the groups and workspace as above. */
+MOE_API moe_status moe_grouped_gemm_dgrad(const moe_product_config *cfg, const int32_t *group_offsets,
+                                          const void *dy, const void *w, void *da, void *ws,
+                                          size_t ws_bytes, cudaStream_t stream);
+
+/* The gradient of the weights, dw_g = sum over rows r of group g of dy[r]^T a[r]: dy
+ * [n_rows, n] bf16, a [n_rows, k] bf16, dw [n_groups, n, k] (cfg->out), zeros for a group
+ * without rows.  Rows outside a group never enter its sum, whatever they hold. */
+MOE_API moe_status moe_grouped_gemm_wgrad(const moe_product_config *cfg, const int32_t *group_offsets,
+                                          const void *dy, const void *a, void *dw, void *ws,
+                                          size_t ws_bytes, cudaStream_t stream);
+
 /* Self-test of the device-side failure path (no counterpart on the pages): a
  * tiny kernel waits on a barrier that nothing completes, gives up after
  * `budget_cycles` SM clock cycles (1 .. 2^33), writes MOE_ERR_TIMEOUT into the

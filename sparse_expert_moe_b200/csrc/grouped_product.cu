@@ -1,0 +1,1212 @@
+// grouped_product.cu -- products grouped by expert, one at a time, on the 5th-generation
+// tensor cores (moe_grouped_gemm, _dgrad, _wgrad): for the rows r of group g
+//   NT  y[r]  = a[r] W_g^T           inner index k
+//   NN  da[r] = dy[r] W_g            inner index n
+//   TN  dW_g  = sum_r dy[r]^T a[r]   inner index r: the rows of the group
+// bf16 operands, or (NT) e4m3 operands with one fp32 scale per 128 inner elements of a row and
+// per 128 x 128 block of a weight,
+//   y[r, j] = sum_b s_a[r, b] s_w[j / 128, b] (sum over block b of a[r, i] w[j, i]),
+// the inner sums on the tensor cores, the outer one in fp32 registers.
+//
+// Two kernels share a scheduler.  Both put the weight index on the MMA's M side (128 lanes of
+// TMEM per CTA) and the group's tokens on its N side, so a group of few rows costs a narrow
+// MMA; TN has the weight's n index on M and its k index on N.
+//
+//   stream_kernel  groups of few rows: HBM-bound on the weights.  One CTA per SM, tiles of
+//                  256 weight rows x 32 tokens.  All tiles' K blocks form one sequence, cut
+//                  into equal contiguous pieces, one per CTA, so every SM streams the same
+//                  number of weight bytes whatever the groups are.
+//   pair_kernel    larger groups, and every TN product: two CTAs share 256 x 256 tiles
+//                  (cta_group::2), each staging 128 rows of either operand, which halves the
+//                  shared-memory fill per flop of 128-row tiles.  Whole rounds of tiles go
+//                  to the pairs in an order that keeps a few weight blocks and token tiles in
+//                  L2; the K blocks of the last, partial round are cut equally as above.
+//
+// A tile whose K blocks fell to several CTAs is joined without waiting: each writes its fp32
+// sums to the workspace, and the one that arrives last (a counter in the workspace header)
+// adds all of them in K order, so that results do not depend on who was last.
+//
+// Warp roles: 0 TMA producer, 1 MMA issuer (and TMEM owner), 2 scales (e4m3) or the zeroing of
+// rows behind a group's last (TN), 3.. epilogue.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+enum Op { kNT = 0, kNN = 1, kTN = 2 };
+
+constexpr int kMaxProductGroups = 1024;
+constexpr uint32_t kBox = 64 * 128;             // one 64-row box of 128-byte rows
+constexpr uint32_t kTileA = 2 * kBox;           // 128 x 128 bytes
+constexpr int kCounterWord0 = 16;               // header words 16..63: four 8-bit counters each
+constexpr int kMaxCounters = 192;
+constexpr int kScaleBlocks = 8;                 // K blocks of scales fetched at a time
+
+struct ProductArgs {
+  CUtensorMap wmap;             // NT, NN: weights [G][n][k]; TN: dy [rows][n]
+  CUtensorMap tmap[4];          // NT, NN: token rows, boxes of 128, 64, 32, 16; TN: [0] a [rows][k]
+  const int32_t* offsets;       // null: one group of all n_rows rows
+  int n_groups, n_rows;
+  int m_total;                  // output index on the M side: NT n, NN k, TN n
+  int n_total;                  // TN: k (the N side)
+  int k_blocks;                 // NT, NN: 128-byte blocks of the inner index
+  void* out;
+  int ld_out;
+  int* header;                  // workspace: status word, counters
+  float* partials;              // workspace: fp32 sums of cut tiles
+  const float *a_scale, *w_scale;   // e4m3: [rows][k_blocks], [G][m blocks][k_blocks]
+  int w_scale_rows;             // 128-row blocks of a weight
+};
+
+// ------------------------------------------------------------------ scheduling
+// Group row offsets and the prefix of the groups' tile counts, in shared memory.
+struct GroupTable {
+  int32_t off[kMaxProductGroups + 1];
+  int32_t pre[kMaxProductGroups + 1];
+};
+
+// Tiles of group rows m: as few as hold at most `width` rows each, of nearly equal size.
+__device__ __forceinline__ int token_tiles(int m, int width) { return (m + width - 1) / width; }
+__device__ __forceinline__ int tile_rows_of(int m, int tiles, int unit) {
+  return ((m + tiles - 1) / tiles + unit - 1) / unit * unit;
+}
+
+// Fills the table; returns the number of tiles (0, with the status set, for bad offsets).
+// `per_group` > 0: that many tiles for every group (TN).  All threads call it.
+__device__ int build_groups(const ProductArgs& p, GroupTable& gt, int width, int m_blocks, int per_group) {
+  const int G = p.n_groups;
+  for (int i = threadIdx.x; i <= G; i += blockDim.x)
+    gt.off[i] = p.offsets ? p.offsets[i] : (i ? p.n_rows : 0);
+  __syncthreads();
+  int bad = 0;
+  for (int i = threadIdx.x; i < G; i += blockDim.x)
+    bad |= gt.off[i] < 0 || gt.off[i + 1] < gt.off[i] || gt.off[i + 1] > p.n_rows;
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) record_status(p.header, kStatusDeviceIndex);
+    return 0;
+  }
+  if (per_group) return per_group * G;
+  if (threadIdx.x < 32) {
+    int carry = 0;
+    for (int b = 0; b < G; b += 32) {
+      const int g = b + threadIdx.x;
+      const int c = g < G ? token_tiles(gt.off[g + 1] - gt.off[g], width) * m_blocks : 0;
+      int incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (static_cast<int>(threadIdx.x) >= o) incl += v;
+      }
+      if (g < G) gt.pre[g] = carry + incl - c;
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (threadIdx.x == 0) gt.pre[G] = carry;
+  }
+  __syncthreads();
+  return gt.pre[G];
+}
+
+struct Tile {
+  int g, mb, nb;                // group, M block, N block (TN)
+  int row0, rows;               // NT, NN: first token row and rows; TN: the group's rows
+};
+
+// Tile t of the NT / NN products: group by group; inside a group, runs of `run` weight blocks
+// sweep all token tiles before the next, so that CTAs at work together share both operands.
+__device__ __forceinline__ Tile token_tile(const GroupTable& gt, int G, int t, int width, int unit,
+                                           int m_blocks, int run) {
+  int lo = 0, hi = G;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (gt.pre[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  Tile c;
+  c.g = lo;
+  const int m = gt.off[lo + 1] - gt.off[lo];
+  const int nt = token_tiles(m, width), per = tile_rows_of(m, nt, unit);
+  const int local = t - gt.pre[lo];
+  const int strip = local / (nt * run);
+  const int wide = min(run, m_blocks - strip * run);
+  const int rem = local - strip * nt * run;
+  const int tok = rem / wide;
+  c.mb = strip * run + rem - tok * wide;
+  c.nb = 0;
+  c.row0 = gt.off[lo] + tok * per;
+  c.rows = min(per, m - tok * per);
+  return c;
+}
+// Tile t of the TN product: runs of `run` M blocks sweep all N blocks.
+__device__ __forceinline__ Tile grad_tile(const GroupTable& gt, int t, int m_blocks, int n_blocks, int run) {
+  Tile c;
+  c.g = t / (m_blocks * n_blocks);
+  const int local = t - c.g * m_blocks * n_blocks;
+  const int strip = local / (n_blocks * run);
+  const int wide = min(run, m_blocks - strip * run);
+  const int rem = local - strip * n_blocks * run;
+  c.nb = rem / wide;
+  c.mb = strip * run + rem - c.nb * wide;
+  c.row0 = gt.off[c.g];
+  c.rows = gt.off[c.g + 1] - c.row0;
+  return c;
+}
+
+// The work of one CTA (or pair) `me` of `n`: first whole tiles me, me + n, ... below `whole`,
+// then its equal share of the K blocks of tiles whole .. n_tiles - 1.
+struct Piece {
+  int tile, kb0, kb1;
+};
+struct Schedule {
+  int me, n, n_tiles, whole, kb;
+  int sharers;                  // CTAs that share the cut tiles' K blocks
+  long long total;              // K blocks of the cut tiles
+  // state
+  int next_whole;
+  long long u, u1;
+
+  __device__ __forceinline__ Schedule(int me_, int n_, int n_tiles_, int whole_, int kb_, int min_blocks)
+      : me(me_), n(n_), n_tiles(n_tiles_), whole(whole_), kb(kb_), next_whole(me_) {
+    total = static_cast<long long>(n_tiles - whole) * kb;
+    const long long most = (total + min_blocks - 1) / min_blocks;
+    sharers = most < n ? static_cast<int>(most) : n;
+    u = u1 = 0;
+    if (me < sharers) {
+      u = total * me / sharers;
+      u1 = total * (me + 1) / sharers;
+    }
+  }
+  __device__ __forceinline__ bool next(Piece& c) {
+    if (next_whole < whole) {
+      c.tile = next_whole;
+      c.kb0 = 0;
+      c.kb1 = kb;
+      next_whole += n;
+      return true;
+    }
+    if (u >= u1) return false;
+    const long long t = u / kb;
+    c.tile = whole + static_cast<int>(t);
+    c.kb0 = static_cast<int>(u - t * kb);
+    const long long left = u1 - u;
+    c.kb1 = left < kb - c.kb0 ? c.kb0 + static_cast<int>(left) : kb;
+    u += c.kb1 - c.kb0;
+    return true;
+  }
+  __device__ __forceinline__ bool cut(const Piece& c) const { return c.kb1 - c.kb0 < kb; }
+  // First and last CTA with a piece of tile t (cut tiles only).
+  __device__ __forceinline__ int owner(long long unit) const {
+    return static_cast<int>(((unit + 1) * sharers - 1) / total);
+  }
+  __device__ __forceinline__ void owners(int t, int& first, int& last) const {
+    const long long b = static_cast<long long>(t - whole) * kb;
+    first = owner(b);
+    last = owner(b + kb - 1);
+  }
+};
+
+// ------------------------------------------------------------------ epilogue pieces
+// A warp's 16 tokens x 32 output columns (lane = column) to rows of `out`: through the warp's
+// shared-memory stage, so that global memory sees 16-byte pieces of rows.  Tokens at or past
+// `rows` and columns at or past `cols` are skipped (cols a multiple of 8).
+template <typename T>
+__device__ __forceinline__ void store_transposed(T* out, size_t ld, int rows, int cols, const float (&v)[16],
+                                                 void* stage_raw, int lane) {
+  T* stage = static_cast<T*>(stage_raw);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if constexpr (sizeof(T) == 4) stage[i * 32 + lane] = v[i];
+    else stage[i * 32 + lane] = __float2bfloat16_rn(v[i]);
+  }
+  __syncwarp();
+  constexpr int kElems = 16 / static_cast<int>(sizeof(T)), kVecs = 32 / kElems;
+#pragma unroll
+  for (int q = lane; q < 16 * kVecs; q += 32) {
+    const int r = q / kVecs, c = (q % kVecs) * kElems;
+    if (r < rows && c < cols)
+      *reinterpret_cast<uint4*>(out + r * ld + c) = *reinterpret_cast<const uint4*>(stage + r * 32 + c);
+  }
+  __syncwarp();
+}
+// A warp's 32 rows (lane = row) x 16 columns to rows of `out`, likewise.
+template <typename T>
+__device__ __forceinline__ void store_direct(T* out, size_t ld, int rows, int cols, const float (&v)[16],
+                                             void* stage_raw, int lane) {
+  constexpr int kElems = 16 / static_cast<int>(sizeof(T)), kVecs = 16 / kElems;   // 16-byte units per row
+  uint4* stage = static_cast<uint4*>(stage_raw);
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    uint4 q;
+    if constexpr (sizeof(T) == 4) {
+      q = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]),
+                     __float_as_uint(v[4 * u + 3]));
+    } else {
+      __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[e] = __floats2bfloat162_rn(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]);
+    }
+    stage[lane * kVecs + (u ^ ((lane * kVecs / 8) & (kVecs - 1)))] = q;   // spread over the banks
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = lane; i < 32 * kVecs; i += 32) {
+    const int r = i / kVecs, u = i % kVecs;
+    if (r < rows && u * kElems < cols)
+      *reinterpret_cast<uint4*>(out + r * ld + u * kElems) =
+          stage[r * kVecs + (u ^ ((r * kVecs / 8) & (kVecs - 1)))];
+  }
+  __syncwarp();
+}
+
+// Barrier between the epilogue warps of a CTA, bounded like every other wait.
+struct EpilogueSync {
+  uint64_t* bar;
+  volatile int* abort_flag;
+  int* status;
+  uint32_t parity = 0;
+  __device__ __forceinline__ bool operator()(int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    const bool ok = mbar_wait(bar, parity, abort_flag, status);
+    parity ^= 1u;
+    return __all_sync(0xffffffffu, ok) != 0;
+  }
+};
+
+// After the epilogue warps have written a cut tile's sums: counts this CTA in and says
+// whether it is the last of `n`.  False in `ok` if a wait ran out.
+__device__ __forceinline__ bool arrive_last(int* header, int counter, int n, EpilogueSync& sync, int* flag,
+                                            bool first_thread, int lane, bool& ok) {
+  __threadfence();                                   // this thread's sums before the count
+  ok = sync(lane);
+  if (!ok) return false;
+  if (first_thread) {
+    unsigned* word = reinterpret_cast<unsigned*>(header) + kCounterWord0 + (counter >> 2);
+    const int sh = 8 * (counter & 3);
+    const unsigned before = (atomicAdd(word, 1u << sh) >> sh) & 0xFFu;
+    const bool last = before == static_cast<unsigned>(n - 1);
+    if (last) atomicSub(word, static_cast<unsigned>(n) << sh);   // left zero for the next call
+    *flag = last;
+  }
+  ok = sync(lane);
+  if (!ok) return false;
+  const bool last = *reinterpret_cast<volatile int*>(flag) != 0;
+  if (last) __threadfence();                         // the others' sums after the count
+  return last;
+}
+
+// ------------------------------------------------------------------ stream kernel
+template <bool F8, int OP>
+struct StreamCfg {
+  static constexpr int kMB = 2;                                   // 128-row weight blocks per tile
+  static constexpr int kNTok = 32;
+  static constexpr uint32_t kA = kMB * kTileA;
+  static constexpr uint32_t kStage = kA + kNTok * 128;
+  static constexpr int kStages = 5;
+  static constexpr int kCols = kMB * kNTok;                       // TMEM columns per buffer
+  static constexpr int kBufs = F8 ? 8 : 2;                        // e4m3: one per K block in flight
+  static constexpr uint32_t kTmem = F8 ? 512 : 128;
+  static constexpr uint32_t kScales = F8 ? 2 * kScaleBlocks * kMB * kNTok * 4 : 0;
+  static constexpr uint32_t kStaging = 4 * 2048;
+  static constexpr size_t kTileFloats = static_cast<size_t>(kMB) * 128 * kNTok;
+  static constexpr uint32_t kSmem =
+      1024 + kStages * kStage + 1024 + kScales + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
+  static_assert(kBufs * kCols <= static_cast<int>(kTmem) && kSmem <= 227 * 1024, "budget");
+};
+
+template <bool F8, int OP, typename OUT>
+__global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ ProductArgs p) {
+  using C = StreamCfg<F8, OP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(tiles + C::kStages * C::kStage);
+  uint64_t* empty_bar = full_bar + C::kStages;
+  uint64_t* tfull_bar = empty_bar + C::kStages;       // [kBufs] accumulators written
+  uint64_t* tempty_bar = tfull_bar + C::kBufs;        // [kBufs] accumulators read
+  uint64_t* sfull_bar = tempty_bar + C::kBufs;        // [2] scales of kScaleBlocks K blocks
+  uint64_t* sempty_bar = sfull_bar + 2;
+  uint64_t* epi_bar = sempty_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* last_flag = reinterpret_cast<int*>(tmem_slot + 2);
+  float* scales = reinterpret_cast<float*>(tiles + C::kStages * C::kStage + 1024);
+  uint8_t* staging = reinterpret_cast<uint8_t*>(scales) + C::kScales;
+  GroupTable& gt = *reinterpret_cast<GroupTable*>(staging + C::kStaging);
+  int* status = p.header;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full_bar[i], 1);
+      mbar_init(&empty_bar[i], 1);
+    }
+    for (int i = 0; i < C::kBufs; ++i) {
+      mbar_init(&tfull_bar[i], 1);
+      mbar_init(&tempty_bar[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull_bar[i], 1);
+      mbar_init(&sempty_bar[i], 4);
+    }
+    mbar_init(epi_bar, 4);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.wmap);
+    tma_prefetch_desc(&p.tmap[2]);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::kTmem);
+    tmem_relinquish();
+  }
+  const int m_blocks = (p.m_total + 128 * C::kMB - 1) / (128 * C::kMB);
+  const int n_tiles = build_groups(p, gt, C::kNTok, m_blocks, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Schedule sched(blockIdx.x, gridDim.x, n_tiles, 0, p.k_blocks, 2);
+  Piece c;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok && sched.next(c)) {
+        const Tile t = token_tile(gt, p.n_groups, c.tile, C::kNTok, 16, m_blocks, 1);
+        const int box = t.rows > 16 ? 32 : 16;
+        const CUtensorMap* tm = &p.tmap[box == 32 ? 2 : 3];
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = tiles + stage * C::kStage;
+          const int kx = kb * (F8 ? 128 : 64);
+          mbar_arrive_expect_tx(&full_bar[stage], C::kA + box * 128);
+          if (OP == kNT) {
+#pragma unroll
+            for (int j = 0; j < C::kMB; ++j)
+              tma_load_3d(st + j * kTileA, &p.wmap, &full_bar[stage], kx, (t.mb * C::kMB + j) * 128, t.g);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2 * C::kMB; ++j)
+              tma_load_3d(st + j * kBox, &p.wmap, &full_bar[stage], t.mb * C::kMB * 128 + j * 64, kx, t.g);
+          }
+          tma_load_2d(st + C::kA, tm, &full_bar[stage], kx, t.row0);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, it = 0;               // accumulator buffers used so far
+      bool ok = true;
+      while (ok && sched.next(c)) {
+        const Tile t = token_tile(gt, p.n_groups, c.tile, C::kNTok, 16, m_blocks, 1);
+        const int n_pad = (t.rows + 15) & ~15;
+        const uint32_t idesc = F8 ? idesc_e4m3_f32(128, n_pad)
+                                  : (idesc_bf16_f32(128, n_pad) | (OP == kNN ? kIdescAMajorMN : 0u));
+        uint32_t d0 = 0, b = 0;
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          if (F8 || kb == c.kb0) {              // a fresh accumulator buffer
+            b = it % C::kBufs;
+            if (!mbar_wait(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status)) {
+              ok = false;
+              break;
+            }
+            d0 = tmem + b * C::kCols;
+            ++it;
+          }
+          if (!mbar_wait(&full_bar[stage], phase, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(tiles) + stage * C::kStage, sb = sa + C::kA;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t bd = umma_desc_sw128(sb + kk * 32);
+            const uint32_t accumulate = (kk || (!F8 && kb > c.kb0)) ? 1u : 0u;
+#pragma unroll
+            for (int j = 0; j < C::kMB; ++j) {
+              const uint32_t aj = sa + j * kTileA;
+              if (F8) umma_e4m3(d0 + j * C::kNTok, umma_desc_sw128(aj + kk * 32), bd, idesc, accumulate);
+              else if (OP == kNT) umma_bf16(d0 + j * C::kNTok, umma_desc_sw128(aj + kk * 32), bd, idesc, accumulate);
+              else umma_bf16(d0 + j * C::kNTok, umma_desc_mn_sw128(aj + kk * 2048), bd, idesc, accumulate);
+            }
+          }
+          umma_commit(&empty_bar[stage]);
+          if (F8) umma_commit(&tfull_bar[b]);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!F8 && ok) umma_commit(&tfull_bar[b]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- scales (e4m3)
+    // For kScaleBlocks K blocks at a time: lane = token fetches its scales, multiplies them by
+    // the weight blocks' and leaves the products as [K block][weight block][token].
+    if (F8) {
+      uint32_t it = 0;
+      bool ok = true;
+      while (ok && sched.next(c)) {
+        const Tile t = token_tile(gt, p.n_groups, c.tile, C::kNTok, 16, m_blocks, 1);
+        const float* sa = p.a_scale + static_cast<size_t>(t.row0 + min(lane, t.rows - 1)) * p.k_blocks;
+        for (int kb = c.kb0; kb < c.kb1; kb += kScaleBlocks, ++it) {
+          const bool w = mbar_wait(&sempty_bar[it & 1], ((it >> 1) & 1u) ^ 1u, abort_flag, status);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          float* dst = scales + (it & 1) * (kScaleBlocks * C::kMB * C::kNTok);
+          float s[kScaleBlocks], ws[C::kMB][kScaleBlocks];
+#pragma unroll
+          for (int q = 0; q < kScaleBlocks; ++q) {
+            const int at = min(kb + q, c.kb1 - 1);
+            s[q] = __ldg(sa + at);
+#pragma unroll
+            for (int j = 0; j < C::kMB; ++j)
+              ws[j][q] = __ldg(p.w_scale + (static_cast<size_t>(t.g) * p.w_scale_rows +
+                                            min(t.mb * C::kMB + j, p.w_scale_rows - 1)) * p.k_blocks + at);
+          }
+#pragma unroll
+          for (int q = 0; q < kScaleBlocks; ++q)
+#pragma unroll
+            for (int j = 0; j < C::kMB; ++j) dst[(q * C::kMB + j) * C::kNTok + lane] = s[q] * ws[j][q];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfull_bar[it & 1]);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- epilogue
+    const int sub = warp & 3;                   // TMEM lane quadrant
+    const int m_local = sub * 32 + lane;
+    uint8_t* stg = staging + sub * 2048;
+    EpilogueSync sync{epi_bar, abort_flag, status};
+    uint32_t it = 0, sit = 0;
+    bool ok = true;
+    while (ok && sched.next(c)) {
+      const Tile t = token_tile(gt, p.n_groups, c.tile, C::kNTok, 16, m_blocks, 1);
+      float acc[C::kMB][2][16];
+      if (F8) {
+#pragma unroll
+        for (int j = 0; j < C::kMB; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[j][0][i] = acc[j][1][i] = 0.f;
+        for (int kb = c.kb0; kb < c.kb1; ++kb, ++it) {
+          const uint32_t b = it % C::kBufs;
+          const int q = (kb - c.kb0) % kScaleBlocks;
+          bool w = true;
+          if (q == 0) w = mbar_wait(&sfull_bar[sit & 1], (sit >> 1) & 1u, abort_flag, status);
+          w = w && mbar_wait(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
+          const float* sc = scales + ((sit & 1) * kScaleBlocks + q) * (C::kMB * C::kNTok);
+#pragma unroll
+          for (int j = 0; j < C::kMB; ++j) {
+            float v0[16], v1[16];
+            if (t.rows > 16) tmem_ld16x2(tb + j * C::kNTok, tb + j * C::kNTok + 16, v0, v1);
+            else tmem_ld16(tb + j * C::kNTok, v0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[j][0][i] = fmaf(sc[j * C::kNTok + i], v0[i], acc[j][0][i]);
+            if (t.rows > 16)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[j][1][i] = fmaf(sc[j * C::kNTok + 16 + i], v1[i], acc[j][1][i]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&tempty_bar[b]);
+            if (q == kScaleBlocks - 1 || kb + 1 == c.kb1) mbar_arrive(&sempty_bar[sit & 1]);
+          }
+          if (q == kScaleBlocks - 1 || kb + 1 == c.kb1) ++sit;
+        }
+        if (!ok) break;
+      } else {
+        const uint32_t b = it % C::kBufs;
+        const bool w = mbar_wait(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
+        if (!__all_sync(0xffffffffu, w)) break;
+        tc_fence_after();
+        const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
+#pragma unroll
+        for (int j = 0; j < C::kMB; ++j) {
+          if (t.rows > 16) tmem_ld16x2(tb + j * C::kNTok, tb + j * C::kNTok + 16, acc[j][0], acc[j][1]);
+          else tmem_ld16(tb + j * C::kNTok, acc[j][0]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty_bar[b]);
+        ++it;
+      }
+      if (sched.cut(c)) {
+        int first, last;
+        sched.owners(c.tile, first, last);
+        auto slot = [&](int cta) {
+          return p.partials + (static_cast<size_t>(cta) * 2 + (cta == first ? 1 : 0)) * C::kTileFloats + m_local;
+        };
+        float* mine = slot(blockIdx.x);
+#pragma unroll
+        for (int j = 0; j < C::kMB; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (h * 16 < t.rows)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) __stcg(mine + (j * C::kNTok + h * 16 + i) * 128, acc[j][h][i]);
+        if (!arrive_last(p.header, first, last - first + 1, sync, last_flag, m_local == 0, lane, ok)) continue;
+#pragma unroll
+        for (int j = 0; j < C::kMB; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[j][0][i] = acc[j][1][i] = 0.f;
+        for (int cta = first; cta <= last; ++cta) {
+          const float* part = slot(cta);
+#pragma unroll
+          for (int j = 0; j < C::kMB; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (h * 16 < t.rows)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[j][h][i] += __ldcg(part + (j * C::kNTok + h * 16 + i) * 128);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < C::kMB; ++j) {
+        const int col0 = (t.mb * C::kMB + j) * 128 + sub * 32;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (h * 16 < t.rows && col0 < p.m_total)
+            store_transposed<OUT>(static_cast<OUT*>(p.out) + static_cast<size_t>(t.row0 + h * 16) * p.ld_out + col0,
+                                  p.ld_out, t.rows - h * 16, p.m_total - col0, acc[j][h], stg, lane);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, C::kTmem);
+}
+
+// ------------------------------------------------------------------ pair kernel
+template <bool F8, int OP>
+struct PairCfg {
+  static constexpr int kWidth = 256;                              // tokens (TN: columns) per tile
+  static constexpr uint32_t kStage = 2 * kTileA;                  // 128 rows of either operand
+  static constexpr int kStages = F8 ? 5 : 6;
+  // bf16: two accumulators of 256 columns; e4m3: four buffers of 128 columns, each holding one
+  // K block's products of half a tile, so that draining one overlaps the MMAs into the others
+  static constexpr int kBufs = F8 ? 4 : 2;
+  static constexpr int kCols = F8 ? 128 : 256;
+  static constexpr int kEpi = F8 ? 8 : 4;                         // epilogue warps
+  static constexpr int kThreads = 32 * (3 + kEpi);
+  static constexpr uint32_t kScales = F8 ? 2 * kScaleBlocks * kWidth * 4 : 0;
+  static constexpr uint32_t kStaging = kEpi * 2048;
+  static constexpr size_t kTileFloats = 2u * 128 * 256;           // both CTAs
+  static constexpr uint32_t kSmem =
+      1024 + kStages * kStage + 1024 + kScales + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
+  static_assert(kSmem <= 227 * 1024, "budget");
+};
+
+// Tokens of half h (128 TMEM columns) of an e4m3 tile, rounded up so that either CTA of the
+// pair loads a multiple of 16 rows of it.
+__device__ __forceinline__ int half_cols(int rows, int h) {
+  const int m = min(128, rows - 128 * h);
+  return m > 0 ? (m + 31) & ~31 : 0;
+}
+
+template <bool F8, int OP, typename OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kThreads, 1)
+    pair_kernel(const __grid_constant__ ProductArgs p) {
+  using C = PairCfg<F8, OP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(tiles + C::kStages * C::kStage);   // the leader's counts
+  uint64_t* empty_bar = full_bar + C::kStages;
+  uint64_t* land_bar = empty_bar + C::kStages;        // TN: this CTA's loads of a stage
+  uint64_t* tfull_bar = land_bar + C::kStages;
+  uint64_t* tempty_bar = tfull_bar + C::kBufs;        // the leader's counts
+  uint64_t* sfull_bar = tempty_bar + C::kBufs;
+  uint64_t* sempty_bar = sfull_bar + 2;
+  uint64_t* epi_bar = sempty_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* last_flag = reinterpret_cast<int*>(tmem_slot + 2);
+  float* scales = reinterpret_cast<float*>(tiles + C::kStages * C::kStage + 1024);
+  uint8_t* staging = reinterpret_cast<uint8_t*>(scales) + C::kScales;
+  GroupTable& gt = *reinterpret_cast<GroupTable*>(staging + C::kStaging);
+  int* status = p.header;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const bool leader = rank == 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full_bar[i], OP == kTN ? 2 : 1);
+      mbar_init(&empty_bar[i], 1);
+      mbar_init(&land_bar[i], 1);
+    }
+    for (int i = 0; i < C::kBufs; ++i) {
+      mbar_init(&tfull_bar[i], 1);
+      mbar_init(&tempty_bar[i], 2 * C::kEpi);          // both CTAs' epilogue warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull_bar[i], 1);
+      mbar_init(&sempty_bar[i], C::kEpi);
+    }
+    mbar_init(epi_bar, C::kEpi);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.wmap);
+    tma_prefetch_desc(&p.tmap[0]);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  const int m_blocks = (p.m_total + 255) / 256;
+  const int n_blocks = OP == kTN ? (p.n_total + 255) / 256 : 1;
+  const int n_tiles = build_groups(p, gt, C::kWidth, m_blocks, OP == kTN ? m_blocks * n_blocks : 0);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  // K blocks of a tile (TN: of the only group, where tiles may be cut), and the tiles of the
+  // last round, whose K blocks are shared out if that round would leave pairs idle
+  const int kb_all = OP == kTN ? (n_tiles ? (gt.off[1] - gt.off[0] + 63) / 64 : 1) : p.k_blocks;
+  const int rest = n_tiles % n_pairs;
+  const bool share = (OP != kTN || p.n_groups == 1) && kb_all >= 8 && rest * 10 < n_pairs * 9;
+  Schedule sched(pair, n_pairs, n_tiles, share ? n_tiles - rest : n_tiles, kb_all, 4);
+  // The next piece of work and its tile; a whole TN tile has its own group's K blocks.
+  Piece c;
+  Tile t;
+  bool cut = false;
+  auto fetch = [&]() {
+    if (!sched.next(c)) return false;
+    t = OP == kTN ? grad_tile(gt, c.tile, m_blocks, n_blocks, 8)
+                  : token_tile(gt, p.n_groups, c.tile, C::kWidth, 32, m_blocks, 8);
+    cut = sched.cut(c);
+    if (OP == kTN && !cut) c.kb1 = (t.rows + 63) / 64;
+    return true;
+  };
+  // TN: columns of the tile, and the MMA's N
+  auto grad_cols = [&]() { return min(256, p.n_total - t.nb * 256); };
+  auto grad_n = [&]() { return grad_cols() > 128 ? 256 : 128; };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- TMA producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok && fetch()) {
+        const int m0 = t.mb * 256 + rank * 128;
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = tiles + stage * C::kStage;
+          uint8_t* bt = st + kTileA;
+          if (OP == kTN) {
+            const int half = grad_n() / 2;                        // columns per CTA: 64 or 128
+            const int y = t.row0 + kb * 64;
+            uint64_t* bar = &land_bar[stage];
+            mbar_arrive_expect_tx(bar, kTileA + half * 128);
+            tma_load_2d(st, &p.wmap, bar, m0, y);
+            tma_load_2d(st + kBox, &p.wmap, bar, m0 + 64, y);
+            for (int x = 0; x < half; x += 64)
+              tma_load_2d(bt + x * 128, &p.tmap[0], bar, t.nb * 256 + rank * half + x, y);
+          } else {
+            const uint32_t bar = mapa_shared(&full_bar[stage], 0);
+            const int kx = kb * (F8 ? 128 : 64);
+            const int n_pad = F8 ? half_cols(t.rows, 0) + half_cols(t.rows, 1) : (t.rows + 31) & ~31;
+            if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kTileA + n_pad * 128);
+            if (OP == kNT) {
+              tma_load_3d_pair(st, &p.wmap, bar, kx, m0, t.g);
+            } else {
+              tma_load_3d_pair(st, &p.wmap, bar, m0, kx, t.g);
+              tma_load_3d_pair(st + kBox, &p.wmap, bar, m0 + 64, kx, t.g);
+            }
+            // this CTA's half of the token rows (e4m3: of either half tile), in boxes of
+            // 128, 64, 32 and 16 rows
+#pragma unroll
+            for (int h = 0; h < (F8 ? 2 : 1); ++h) {
+              const int rows = (F8 ? half_cols(t.rows, h) : n_pad) / 2;
+              const int y = t.row0 + h * 128 + rank * rows;
+              for (int bi = 0, off = 0; bi < 4; ++bi) {
+                const int box = 128 >> bi;
+                while (rows - off >= box) {
+                  tma_load_2d_pair(bt + h * kBox + off * 128, &p.tmap[bi], bar, kx, y + off);
+                  off += box;
+                }
+              }
+            }
+          }
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer (the leader)
+    if (lane == 0 && leader) {
+      int stage = 0;
+      uint32_t phase = 0, it = 0;
+      bool ok = true;
+      while (ok && fetch()) {
+        if (c.kb1 <= c.kb0) continue;                             // TN: a group without rows
+        uint32_t b = 0;
+        if (!F8) {
+          b = it % C::kBufs;
+          if (!mbar_wait_cluster(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status)) break;
+          ++it;
+        }
+        const int n_pad = OP == kTN ? grad_n() : (t.rows + 31) & ~31;
+        const uint32_t idesc = idesc_bf16_f32(256, n_pad) | (OP != kNT ? kIdescAMajorMN : 0u) |
+                               (OP == kTN ? kIdescBMajorMN : 0u);
+        for (int kb = c.kb0; kb < c.kb1 && ok; ++kb) {
+          ok = OP == kTN ? mbar_wait_cluster(&full_bar[stage], phase, abort_flag, status)
+                         : mbar_wait(&full_bar[stage], phase, abort_flag, status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(tiles) + stage * C::kStage, sb = sa + kTileA;
+          if (F8) {
+            const int halves = t.rows > 128 ? 2 : 1;
+            for (int h = 0; h < halves; ++h, ++it) {
+              b = it % C::kBufs;
+              ok = mbar_wait_cluster(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status);
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t id8 = idesc_e4m3_f32(256, half_cols(t.rows, h));
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_e4m3_pair(tmem + b * C::kCols, umma_desc_sw128(sa + kk * 32),
+                               umma_desc_sw128(sb + h * kBox + kk * 32), id8, kk ? 1u : 0u);
+              if (h + 1 == halves) umma_commit_pair(&empty_bar[stage], 0x3);
+              umma_commit_pair(&tfull_bar[b], 0x3);
+            }
+          } else {
+            const int left = OP == kTN ? t.rows - kb * 64 : 64;
+            const int steps = left < 64 ? (left + 15) / 16 : 4;
+            const uint32_t d = tmem + b * C::kCols;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk >= steps) break;
+              const uint64_t ad = OP == kNT ? umma_desc_sw128(sa + kk * 32) : umma_desc_mn_sw128(sa + kk * 2048);
+              const uint64_t bd = OP == kTN ? umma_desc_mn_sw128(sb + kk * 2048) : umma_desc_sw128(sb + kk * 32);
+              umma_bf16_pair(d, ad, bd, idesc, (kb > c.kb0 || kk) ? 1u : 0u);
+            }
+            umma_commit_pair(&empty_bar[stage], 0x3);
+          }
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!F8 && ok) umma_commit_pair(&tfull_bar[b], 0x3);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    if (F8) {
+      // -------------------------------------------------------- scales (e4m3, both CTAs)
+      // For kScaleBlocks K blocks at a time: each token's scales times this CTA's weight
+      // block's, as [K block][token].
+      uint32_t it = 0;
+      bool ok = true;
+      while (ok && fetch()) {
+        const float* sw = p.w_scale + (static_cast<size_t>(t.g) * p.w_scale_rows +
+                                       min(2 * t.mb + rank, p.w_scale_rows - 1)) * p.k_blocks;
+        for (int kb = c.kb0; kb < c.kb1; kb += kScaleBlocks, ++it) {
+          const bool w = mbar_wait(&sempty_bar[it & 1], ((it >> 1) & 1u) ^ 1u, abort_flag, status);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          float* dst = scales + (it & 1) * (kScaleBlocks * C::kWidth);
+          float ws[kScaleBlocks];
+#pragma unroll
+          for (int q = 0; q < kScaleBlocks; ++q) ws[q] = __ldg(sw + min(kb + q, c.kb1 - 1));
+          for (int n0 = 0; n0 < t.rows; n0 += 128) {
+            float s[4][kScaleBlocks];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float* sa = p.a_scale +
+                                static_cast<size_t>(t.row0 + min(n0 + j * 32 + lane, t.rows - 1)) * p.k_blocks;
+#pragma unroll
+              for (int q = 0; q < kScaleBlocks; ++q) s[j][q] = __ldg(sa + min(kb + q, c.kb1 - 1));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int q = 0; q < kScaleBlocks; ++q) dst[q * C::kWidth + n0 + j * 32 + lane] = s[j][q] * ws[q];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfull_bar[it & 1]);
+        }
+      }
+    } else if (OP == kTN) {
+      // -------------------------------------------------------- rows behind the group's last
+      // The last K block's rows past the group belong to the next group (or to nobody): in both
+      // operands they are overwritten with zeros up to the MMA's 16-row step.  Then this CTA's
+      // half of the stage is ready: the leader's barrier counts both.
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok && fetch()) {
+        const int boxes = 2 + grad_n() / 128;
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          const bool w = mbar_wait(&land_bar[stage], phase, abort_flag, status);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          const int left = t.rows - kb * 64;
+          if (left < 64 && (left & 15)) {
+            uint8_t* st = tiles + stage * C::kStage;
+            const int units = (16 - (left & 15)) * 8;             // 16-byte pieces per box
+            for (int i = lane; i < units * boxes; i += 32) {
+              const int box = i / units;
+              *reinterpret_cast<uint4*>(st + box * kBox + left * 128 + (i - box * units) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(&full_bar[stage], 0));
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------- epilogue (both CTAs)
+    const int sub = warp & 3;                    // TMEM lane quadrant
+    const int part = (warp - 3) >> 2;            // e4m3: 64-column half of every buffer
+    const int m_local = sub * 32 + lane;
+    uint8_t* stg = staging + (warp - 3) * 2048;
+    EpilogueSync sync{epi_bar, abort_flag, status};
+    uint32_t it = 0, sit = 0;
+    bool ok = true;
+    auto release = [&](uint32_t b) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty_bar[b], 0));
+    };
+    while (ok && fetch()) {
+      const int m0 = t.mb * 256 + rank * 128 + sub * 32;          // the warp's first output index
+      const int cols = OP == kTN ? grad_cols() : t.rows;          // TMEM columns in use
+      int first = 0, last = 0;
+      if (cut) sched.owners(c.tile, first, last);
+      auto slot = [&](int owner) {
+        return p.partials +
+               ((static_cast<size_t>(owner) * 2 + (owner == first ? 1 : 0)) * 2 + rank) * (128 * 256) + m_local;
+      };
+      // sixteen columns of the finished tile to global memory
+      auto finish = [&](const float (&v)[16], int n0) {
+        if (m0 >= p.m_total) return;
+        if (OP == kTN)
+          store_direct<OUT>(static_cast<OUT*>(p.out) + (static_cast<size_t>(t.g) * p.m_total + m0) * p.ld_out +
+                                t.nb * 256 + n0,
+                            p.ld_out, p.m_total - m0, cols - n0, v, stg, lane);
+        else
+          store_transposed<OUT>(static_cast<OUT*>(p.out) + static_cast<size_t>(t.row0 + n0) * p.ld_out + m0,
+                                p.ld_out, cols - n0, p.m_total - m0, v, stg, lane);
+      };
+      auto emit = [&](const float (&v)[16], int n0) {
+        if (!cut) {
+          finish(v, n0);
+        } else {
+          float* mine = slot(pair);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) __stcg(mine + (n0 + i) * 128, v[i]);
+        }
+      };
+      if (F8) {
+        float acc[2][4][16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[h][q][i] = 0.f;
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          const int kq = (kb - c.kb0) % kScaleBlocks;
+          if (kq == 0) {
+            const bool w = mbar_wait(&sfull_bar[sit & 1], (sit >> 1) & 1u, abort_flag, status);
+            ok = __all_sync(0xffffffffu, w) != 0;
+            if (!ok) break;
+          }
+          const float* sc = scales + ((sit & 1) * kScaleBlocks + kq) * C::kWidth + part * 64;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h * 128 >= t.rows) break;
+            const uint32_t b = it % C::kBufs;
+            const bool w = mbar_wait(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
+            ok = __all_sync(0xffffffffu, w) != 0;
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols + part * 64;
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+              if (h * 128 + part * 64 + q * 16 < t.rows) {
+                float v0[16], v1[16];
+                tmem_ld16x2(tb + q * 16, tb + q * 16 + 16, v0, v1);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  acc[h][q][i] = fmaf(sc[h * 128 + q * 16 + i], v0[i], acc[h][q][i]);
+                  acc[h][q + 1][i] = fmaf(sc[h * 128 + q * 16 + 16 + i], v1[i], acc[h][q + 1][i]);
+                }
+              }
+            }
+            release(b);
+            ++it;
+          }
+          if (!ok) break;
+          if (kq == kScaleBlocks - 1 || kb + 1 == c.kb1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sempty_bar[sit & 1]);
+            ++sit;
+          }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (h * 128 + part * 64 + q * 16 < t.rows) emit(acc[h][q], h * 128 + part * 64 + q * 16);
+      } else if (c.kb1 > c.kb0) {
+        const uint32_t b = it % C::kBufs;
+        const bool w = mbar_wait(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
+        if (!__all_sync(0xffffffffu, w)) break;
+        tc_fence_after();
+        const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
+        for (int n0 = 0; n0 < cols; n0 += 16) {
+          float v[16];
+          tmem_ld16(tb + n0, v);
+          emit(v, n0);
+        }
+        release(b);
+        ++it;
+      } else {                                   // TN: a group without rows
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+        for (int n0 = 0; n0 < cols; n0 += 16) finish(v, n0);
+      }
+      if (!cut) continue;
+      if (!arrive_last(p.header, 2 * first + rank, last - first + 1, sync, last_flag, warp == 4 && lane == 0, lane,
+                       ok))
+        continue;
+      for (int n0 = part * 64; n0 < cols; n0 += 16) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+        for (int owner = first; owner <= last; ++owner) {
+          const float* from = slot(owner);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] += __ldcg(from + (n0 + i) * 128);
+        }
+        finish(v, n0);
+        if (F8 && (n0 & 63) == 48) n0 += 64;     // the other warps' 64 columns
+      }
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ------------------------------------------------------------------ host
+constexpr size_t kProductHeader = 256;
+constexpr int kStreamCtas = 148, kPairs = 74;   // most CTAs / pairs a launch uses
+static_assert(kStreamCtas <= kMaxCounters && 2 * kPairs <= kMaxCounters, "join counters");
+
+size_t product_workspace() {
+  const size_t stream = sizeof(float) * 2 * kStreamCtas * StreamCfg<true, kNT>::kTileFloats;
+  const size_t pair = sizeof(float) * 2 * kPairs * PairCfg<false, kNT>::kTileFloats;
+  return kProductHeader + (stream > pair ? stream : pair);
+}
+
+int device_sms() {
+  static int cached[64] = {};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64 && cached[dev]) return cached[dev];
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) cached[dev] = n;
+  return n;
+}
+
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+moe_status check_product(const moe_product_config* c) {
+  if (!c || c->n_groups <= 0 || c->n_rows < 0 || c->n <= 0 || c->k <= 0) return MOE_ERR_INVALID_ARG;
+  if (c->n_groups > kMaxProductGroups || c->n > 65536 || c->k > 65536 || c->n_rows > (1 << 24))
+    return MOE_ERR_UNSUPPORTED;
+  if (c->in != MOE_BF16 && c->in != MOE_E4M3_FP32_SCALE) return MOE_ERR_UNSUPPORTED;
+  if (c->out != MOE_BF16 && c->out != MOE_F32) return MOE_ERR_UNSUPPORTED;
+  if (c->n % 8 || c->k % (c->in == MOE_BF16 ? 8 : 16)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+template <class K>
+cudaError_t launch_product_kernel(K kernel, const ProductArgs& a, int grid, int threads, uint32_t smem,
+                                  cudaStream_t s) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, threads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool F8, int OP, typename OUT>
+cudaError_t launch_product(const ProductArgs& a, bool stream_tiles, cudaStream_t s) {
+  const int sms = device_sms();
+  if (sms < 2) return cudaErrorInvalidDevice;
+  if constexpr (OP != kTN) {
+    if (stream_tiles)
+      return launch_product_kernel(stream_kernel<F8, OP, OUT>, a, sms < kStreamCtas ? sms : kStreamCtas, 224,
+                                   StreamCfg<F8, OP>::kSmem, s);
+  }
+  const int pairs = sms / 2 < kPairs ? sms / 2 : kPairs;
+  return launch_product_kernel(pair_kernel<F8, OP, OUT>, a, 2 * pairs, PairCfg<F8, OP>::kThreads,
+                               PairCfg<F8, OP>::kSmem, s);
+}
+template <bool F8, int OP>
+moe_status launch_product(const ProductArgs& a, bool f32, bool stream_tiles, cudaStream_t s) {
+  const cudaError_t e = f32 ? launch_product<F8, OP, float>(a, stream_tiles, s)
+                            : launch_product<F8, OP, __nv_bfloat16>(a, stream_tiles, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// Groups of few rows go to the stream kernel (only the average is known on the host).
+bool few_rows(const moe_product_config& c) { return c.n_rows <= 32 * c.n_groups; }
+
+moe_status common_checks(const moe_product_config* cfg, const int32_t* offsets, const void* x, const void* y,
+                         const void* z, const void* ws, size_t ws_bytes) {
+  const moe_status st = check_product(cfg);
+  if (st != MOE_OK) return st;
+  if (!ws || (!offsets && cfg->n_groups != 1)) return MOE_ERR_INVALID_ARG;
+  if (misaligned(x) || misaligned(y) || misaligned(z) || misaligned(ws)) return MOE_ERR_INVALID_ARG;
+  return ws_bytes < product_workspace() ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+ProductArgs product_args(const moe_product_config& c, const int32_t* offsets, void* out, void* ws) {
+  ProductArgs a{};
+  a.offsets = offsets;
+  a.n_groups = c.n_groups;
+  a.n_rows = c.n_rows;
+  a.out = out;
+  a.header = static_cast<int*>(ws);
+  a.partials = reinterpret_cast<float*>(static_cast<char*>(ws) + kProductHeader);
+  return a;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_product_workspace_size(const moe_product_config* cfg, size_t* bytes) {
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  const moe_status st = check_product(cfg);
+  if (st != MOE_OK) return st;
+  *bytes = product_workspace();
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm(const moe_product_config* cfg, const int32_t* group_offsets, const void* a,
+                            const float* a_scale, const void* w, const float* w_scale, void* y, void* ws,
+                            size_t ws_bytes, cudaStream_t stream) {
+  const moe_status st = common_checks(cfg, group_offsets, a, w, y, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  const bool f8 = cfg->in == MOE_E4M3_FP32_SCALE;
+  if (!f8 && (a_scale || w_scale)) return MOE_ERR_INVALID_ARG;
+  if (cfg->n_rows == 0) return MOE_OK;
+  if (!a || !w || !y || (f8 && (!a_scale || !w_scale))) return MOE_ERR_INVALID_ARG;
+  ProductArgs p = product_args(*cfg, group_offsets, y, ws);
+  bool ok = make_tmap_matrix(&p.wmap, w, f8, cfg->n_groups, cfg->n, cfg->k, 128);
+  for (int i = 0; i < 4 && ok; ++i)
+    ok = f8 ? make_tmap_u8(&p.tmap[i], a, cfg->n_rows, cfg->k, 128u >> i)
+            : make_tmap_bf16(&p.tmap[i], a, cfg->n_rows, cfg->k, 128u >> i);
+  if (!ok) return MOE_ERR_CUDA;
+  p.m_total = p.ld_out = cfg->n;
+  p.k_blocks = (cfg->k + (f8 ? 127 : 63)) / (f8 ? 128 : 64);
+  p.a_scale = a_scale;
+  p.w_scale = w_scale;
+  p.w_scale_rows = (cfg->n + 127) / 128;
+  const bool f32 = cfg->out == MOE_F32;
+  return f8 ? launch_product<true, kNT>(p, f32, few_rows(*cfg), stream)
+            : launch_product<false, kNT>(p, f32, few_rows(*cfg), stream);
+}
+
+moe_status moe_grouped_gemm_dgrad(const moe_product_config* cfg, const int32_t* group_offsets, const void* dy,
+                                  const void* w, void* da, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const moe_status st = common_checks(cfg, group_offsets, dy, w, da, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (cfg->in != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (cfg->n_rows == 0) return MOE_OK;
+  if (!dy || !w || !da) return MOE_ERR_INVALID_ARG;
+  ProductArgs p = product_args(*cfg, group_offsets, da, ws);
+  bool ok = make_tmap_matrix(&p.wmap, w, false, cfg->n_groups, cfg->n, cfg->k, 64);
+  for (int i = 0; i < 4 && ok; ++i) ok = make_tmap_bf16(&p.tmap[i], dy, cfg->n_rows, cfg->n, 128u >> i);
+  if (!ok) return MOE_ERR_CUDA;
+  p.m_total = p.ld_out = cfg->k;
+  p.k_blocks = (cfg->n + 63) / 64;
+  return launch_product<false, kNN>(p, cfg->out == MOE_F32, few_rows(*cfg), stream);
+}
+
+moe_status moe_grouped_gemm_wgrad(const moe_product_config* cfg, const int32_t* group_offsets, const void* dy,
+                                  const void* a, void* dw, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const moe_status st = common_checks(cfg, group_offsets, dy, a, dw, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (cfg->in != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!dw) return MOE_ERR_INVALID_ARG;
+  if (cfg->n_rows == 0) {                        // no rows: every sum is empty
+    const size_t bytes = static_cast<size_t>(cfg->n_groups) * cfg->n * cfg->k * (cfg->out == MOE_F32 ? 4 : 2);
+    return cudaMemsetAsync(dw, 0, bytes, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  if (!dy || !a) return MOE_ERR_INVALID_ARG;
+  ProductArgs p = product_args(*cfg, group_offsets, dw, ws);
+  if (!make_tmap_bf16(&p.wmap, dy, cfg->n_rows, cfg->n, 64) ||
+      !make_tmap_bf16(&p.tmap[0], a, cfg->n_rows, cfg->k, 64))
+    return MOE_ERR_CUDA;
+  p.m_total = cfg->n;
+  p.n_total = p.ld_out = cfg->k;
+  p.k_blocks = 0;
+  return launch_product<false, kTN>(p, cfg->out == MOE_F32, false, stream);
+}
+
+}  // extern "C"

@@ -162,6 +162,11 @@ bool make_tmap_bf16(CUtensorMap* map, const void* base, uint64_t rows, uint64_t 
 // Same for 1-byte (e4m3) elements, box {128 columns, box_rows rows}.
 bool make_tmap_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                   uint32_t box_rows);
+// Row-major matrices [groups][rows, cols] of 2-byte (or 1-byte, u8) elements, box {128 bytes
+// of columns, box_rows rows, one matrix}, 128-byte swizzle: reads past a matrix's rows or
+// columns give zeros, not the next matrix.  The row pitch must be a multiple of 16 bytes.
+bool make_tmap_matrix(CUtensorMap* map, const void* base, bool u8, uint64_t groups, uint64_t rows,
+                      uint64_t cols, uint32_t box_rows);
 // Packed FP4 (two E2M1 codes per byte, `cols` elements per row), box {128 elements,
 // box_rows rows}, loaded into shared memory unpacked to one 16-byte slot per 16 elements
 // (8 data bytes, 8 bytes of gap): the e4m3 tile layout the block-scaled MMA reads FP4

@@ -25,6 +25,7 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 4: "MOE_ERR_CUDA", 5: "MOE_ERR_DEVICE_INDEX", 6: "MOE_ERR_TIMEOUT",
                 7: "MOE_ERR_DEVICE_VALUE"}
 SCORE = {"softmax": 0, "sigmoid_bias": 1}
+GATE = {"none": 0, "channel": 1, "token": 2, "full": 3}
 DTYPE = {"f32": 0, "bf16": 1, "e4m3": 2, "e2m1": 3, "e4m3_fs": 4}
 
 
@@ -44,6 +45,18 @@ class MoeConfig(ctypes.Structure):
 class MoeWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("wr", "sel_bias", "w13", "w2", "w13_s", "w2_s",
                                                 "ws13", "ws2", "ws13_s", "ws2_s")]
+
+
+class MoeNormConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d_model", ctypes.c_int32), ("gate", ctypes.c_int),
+                ("res", ctypes.c_int), ("act", ctypes.c_int), ("weight", ctypes.c_int),
+                ("out", ctypes.c_int), ("eps", ctypes.c_float), ("res_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("w_offset", ctypes.c_float)]
+
+
+class MoeProductConfig(ctypes.Structure):
+    _fields_ = [("n_groups", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("k", ctypes.c_int32), ("in_", ctypes.c_int), ("out", ctypes.c_int)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -77,6 +90,13 @@ def load_library() -> ctypes.CDLL:
                                    ctypes.POINTER(ctypes.c_void_p)],
         "moe_layer_graph_launch": [P, P],
         "moe_layer_graph_destroy": [P],
+        "moe_norm_workspace_size": [ctypes.POINTER(MoeNormConfig), ctypes.POINTER(SZ)],
+        "moe_block_norm": [ctypes.POINTER(MoeNormConfig)] + [P] * 9,
+        "moe_block_norm_backward": [ctypes.POINTER(MoeNormConfig)] + [P] * 13 + [SZ, P],
+        "moe_product_workspace_size": [ctypes.POINTER(MoeProductConfig), ctypes.POINTER(SZ)],
+        "moe_grouped_gemm": [ctypes.POINTER(MoeProductConfig)] + [P] * 7 + [SZ, P],
+        "moe_grouped_gemm_dgrad": [ctypes.POINTER(MoeProductConfig)] + [P] * 5 + [SZ, P],
+        "moe_grouped_gemm_wgrad": [ctypes.POINTER(MoeProductConfig)] + [P] * 5 + [SZ, P],
     }
     for name, argtypes in sigs.items():
         fn = getattr(lib, name)
@@ -246,6 +266,145 @@ def moe_selftest_bounded_wait(ws, budget_cycles, stream=None):
 
 def moe_status_string(code: int) -> str:
     return load_library().moe_status_string(code).decode()
+
+
+# ---------------------------------------------------------------------------
+# norms around a block; products grouped by expert
+# ---------------------------------------------------------------------------
+
+_VALUE_TYPES = {0: torch.float32, 1: torch.bfloat16, 2: torch.float8_e4m3fn, 4: torch.float8_e4m3fn}
+
+
+class _Args:
+    """Checks the tensors of one call (type, size, contiguous, one device) on their way to
+    pointers, and finds the device and stream the call runs on.  Plain integers pass as
+    device addresses."""
+
+    __slots__ = ("fn", "device")
+
+    def __init__(self, fn: str):
+        self.fn, self.device = fn, -1
+
+    def __call__(self, name: str, t, code: int, numel: int):
+        if t is None or isinstance(t, int):
+            return t
+        want = _VALUE_TYPES.get(code)      # None: a type the library refuses by itself
+        if want is not None and t.dtype is not want and not (code in (2, 4) and t.dtype is torch.uint8):
+            raise TypeError(f"{self.fn}: {name} is {t.dtype}, not {want}")
+        return self.raw(name, t, numel)
+
+    def raw(self, name: str, t, numel: int):
+        if t is None or isinstance(t, int):
+            return t
+        if t.numel() != numel or not t.is_contiguous():
+            raise ValueError(f"{self.fn}: {name} must be contiguous with {numel} elements, got shape "
+                             f"{tuple(t.shape)}, strides {t.stride()}")
+        d = t.get_device()
+        if d != self.device or d < 0:
+            if d < 0 or self.device >= 0:
+                raise ValueError(f"{self.fn}: {name} is not on the CUDA device of the other tensors")
+            self.device = d
+        return t.data_ptr()
+
+    def offsets(self, t, n_groups: int):
+        if t is not None and not isinstance(t, int) and t.dtype is not torch.int32:
+            raise TypeError(f"{self.fn}: group_offsets is {t.dtype}, not torch.int32")
+        return self.raw("group_offsets", t, n_groups + 1)
+
+    def workspace(self, ws):
+        if isinstance(ws, int) or ws is None:
+            raise TypeError(f"{self.fn}: the workspace is a tensor")
+        return self.raw("ws", ws, ws.numel()), ws.numel() * ws.element_size()
+
+    def run(self, stream, *args):
+        """The C call on the tensors' device, on `stream` or that device's current stream."""
+        fn = getattr(load_library(), self.fn)
+        if self.device < 0 or self.device == torch.cuda.current_device():
+            _check(self.fn, fn(*args, _stream(stream)))
+        else:
+            with torch.cuda.device(self.device):
+                _check(self.fn, fn(*args, _stream(stream)))
+
+
+def make_norm_config(T, d_model, gate="none", res="bf16", act="bf16", weight="bf16", out="bf16", eps=1e-6,
+                     res_scale=1.0, branch_scale=1.0, w_offset=0.0) -> MoeNormConfig:
+    return MoeNormConfig(T, d_model, GATE[gate], DTYPE[res], DTYPE[act], DTYPE[weight], DTYPE[out], eps,
+                         res_scale, branch_scale, w_offset)
+
+
+def moe_norm_workspace_size(cfg: MoeNormConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_norm_workspace_size",
+           load_library().moe_norm_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def _gate_shape(cfg: MoeNormConfig):
+    """(elements, type code) of the gate."""
+    if cfg.gate == GATE["full"]:
+        return cfg.T * cfg.d_model, cfg.act
+    return (cfg.T if cfg.gate == GATE["token"] else cfg.d_model), cfg.weight
+
+
+def moe_block_norm(cfg: MoeNormConfig, r, y, w_post, gate, w_pre, r_out, h, h_scale, stream=None):
+    """r_out = res_scale r + branch_scale gate norm(y; w_post), h = norm(r_out; w_pre); see
+    include/moe.h for what may be None."""
+    a = _Args("moe_block_norm")
+    d, n = cfg.d_model, cfg.T * cfg.d_model
+    gn, gt = _gate_shape(cfg)
+    a.run(stream, ctypes.byref(cfg), a("r", r, cfg.res, n), a("y", y, cfg.act, n),
+          a("w_post", w_post, cfg.weight, d), a("gate", gate, gt, gn), a("w_pre", w_pre, cfg.weight, d),
+          a("r_out", r_out, cfg.res, n), a("h", h, cfg.out, n), a("h_scale", h_scale, 0, n // 128))
+
+
+def moe_block_norm_backward(cfg: MoeNormConfig, r_out, y, w_post, gate, w_pre, dh, dr_out, dr, dy, dgate,
+                            dw_post, dw_pre, ws, stream=None):
+    """Gradients of moe_block_norm (dr, dy and, where not None, dgate, dw_post, dw_pre)."""
+    a = _Args("moe_block_norm_backward")
+    d, n = cfg.d_model, cfg.T * cfg.d_model
+    gn, gt = _gate_shape(cfg)
+    a.run(stream, ctypes.byref(cfg), a("r_out", r_out, cfg.res, n), a("y", y, cfg.act, n),
+          a("w_post", w_post, cfg.weight, d), a("gate", gate, gt, gn), a("w_pre", w_pre, cfg.weight, d),
+          a("dh", dh, cfg.act, n), a("dr_out", dr_out, cfg.res, n), a("dr", dr, cfg.res, n),
+          a("dy", dy, cfg.act, n), a("dgate", dgate, gt if cfg.gate == GATE["full"] else 0, gn),
+          a("dw_post", dw_post, 0, d), a("dw_pre", dw_pre, 0, d), *a.workspace(ws))
+
+
+def make_product_config(n_groups, n_rows, n, k, dtype="bf16", out="bf16") -> MoeProductConfig:
+    return MoeProductConfig(n_groups, n_rows, n, k, DTYPE[dtype], DTYPE[out])
+
+
+def moe_product_workspace_size(cfg: MoeProductConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_product_workspace_size",
+           load_library().moe_product_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def moe_grouped_gemm(cfg: MoeProductConfig, group_offsets, a, a_scale, w, w_scale, y, ws, stream=None):
+    """y[r] = a[r] W_g^T for the rows r of group g (bf16, or e4m3 with block scales)."""
+    c = _Args("moe_grouped_gemm")
+    G, R, n, k = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k
+    kb, nb = (k + 127) // 128, (n + 127) // 128
+    c.run(stream, ctypes.byref(cfg), c.offsets(group_offsets, G), c("a", a, cfg.in_, R * k),
+          c("a_scale", a_scale, 0, R * kb), c("w", w, cfg.in_, G * n * k),
+          c("w_scale", w_scale, 0, G * nb * kb), c("y", y, cfg.out, R * n), *c.workspace(ws))
+
+
+def moe_grouped_gemm_dgrad(cfg: MoeProductConfig, group_offsets, dy, w, da, ws, stream=None):
+    """da[r] = dy[r] W_g: the gradient of moe_grouped_gemm's rows."""
+    c = _Args("moe_grouped_gemm_dgrad")
+    G, R, n, k = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k
+    c.run(stream, ctypes.byref(cfg), c.offsets(group_offsets, G), c("dy", dy, cfg.in_, R * n),
+          c("w", w, cfg.in_, G * n * k), c("da", da, cfg.out, R * k), *c.workspace(ws))
+
+
+def moe_grouped_gemm_wgrad(cfg: MoeProductConfig, group_offsets, dy, a, dw, ws, stream=None):
+    """dw_g = sum of dy[r]^T a[r] over the rows of group g: the gradient of the weights."""
+    c = _Args("moe_grouped_gemm_wgrad")
+    G, R, n, k = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k
+    c.run(stream, ctypes.byref(cfg), c.offsets(group_offsets, G), c("dy", dy, cfg.in_, R * n),
+          c("a", a, cfg.in_, R * k), c("dw", dw, cfg.out, G * n * k), *c.workspace(ws))
 
 
 # ---------------------------------------------------------------------------
