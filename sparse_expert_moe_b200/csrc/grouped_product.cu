@@ -919,7 +919,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
     auto release = [&](uint32_t b) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty_bar[b], 0));
+      if (lane == 0) mbar_arrive_cluster_light(mapa_shared(&tempty_bar[b], 0));
     };
     while (ok && fetch()) {
       const int m0 = t.mb * 256 + rank * 128 + sub * 32;          // the warp's first output index

@@ -375,6 +375,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same with release semantics inside this CTA only: enough where nothing but finished
+// TMEM loads has to be ordered before it, and without the fence that the cluster-wide form
+// puts behind all of the thread's stores.
+__device__ __forceinline__ void mbar_arrive_cluster_light(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // mbar_wait on a barrier of this CTA that threads of the peer CTA arrive on.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
                                                   volatile int* abort_flag, int* status) {
