@@ -155,24 +155,19 @@ __device__ __forceinline__ Tile grad_tile(const GroupTable& gt, int t, int m_blo
   return c;
 }
 
-// The work of one CTA (or pair) `me` of `n`: first whole tiles me, me + n, ... below `whole`,
-// then its equal share of the K blocks of tiles whole .. n_tiles - 1.
+// A run of K blocks of one tile.
 struct Piece {
   int tile, kb0, kb1;
 };
-struct Schedule {
-  int me, n, n_tiles, whole, kb;
-  int sharers;                  // CTAs that share the cut tiles' K blocks
-  long long total;              // K blocks of the cut tiles
-  // state
-  int next_whole;
-  long long u, u1;
 
-  __device__ __forceinline__ Schedule(int me_, int n_, int n_tiles_, int whole_, int kb_, int min_blocks)
-      : me(me_), n(n_), n_tiles(n_tiles_), whole(whole_), kb(kb_), next_whole(me_) {
-    total = static_cast<long long>(n_tiles - whole) * kb;
-    const long long most = (total + min_blocks - 1) / min_blocks;
-    sharers = most < n ? static_cast<int>(most) : n;
+// Stream kernel: the K blocks of all tiles as one sequence, cut into `sharers` equal pieces.
+struct EvenShare {
+  int kb, sharers;
+  long long total, u, u1;
+
+  __device__ __forceinline__ EvenShare(int me, int n, int n_tiles, int kb_) : kb(kb_) {
+    total = static_cast<long long>(n_tiles) * kb;
+    sharers = (total + 1) / 2 < n ? static_cast<int>((total + 1) / 2) : n;   // two K blocks at least
     u = u1 = 0;
     if (me < sharers) {
       u = total * me / sharers;
@@ -180,16 +175,9 @@ struct Schedule {
     }
   }
   __device__ __forceinline__ bool next(Piece& c) {
-    if (next_whole < whole) {
-      c.tile = next_whole;
-      c.kb0 = 0;
-      c.kb1 = kb;
-      next_whole += n;
-      return true;
-    }
     if (u >= u1) return false;
     const long long t = u / kb;
-    c.tile = whole + static_cast<int>(t);
+    c.tile = static_cast<int>(t);
     c.kb0 = static_cast<int>(u - t * kb);
     const long long left = u1 - u;
     c.kb1 = left < kb - c.kb0 ? c.kb0 + static_cast<int>(left) : kb;
@@ -197,14 +185,57 @@ struct Schedule {
     return true;
   }
   __device__ __forceinline__ bool cut(const Piece& c) const { return c.kb1 - c.kb0 < kb; }
-  // First and last CTA with a piece of tile t (cut tiles only).
+  // First and last CTA with a piece of tile t.
   __device__ __forceinline__ int owner(long long unit) const {
     return static_cast<int>(((unit + 1) * sharers - 1) / total);
   }
   __device__ __forceinline__ void owners(int t, int& first, int& last) const {
-    const long long b = static_cast<long long>(t - whole) * kb;
+    const long long b = static_cast<long long>(t) * kb;
     first = owner(b);
     last = owner(b + kb - 1);
+  }
+};
+
+// Pair kernel: whole tiles me, me + n, ...; the tiles of a last round that would leave at least
+// half of the pairs idle are cut into `parts` equal runs of K blocks, one per pair.  Joining a
+// 256 x 256 tile costs about eight K blocks' time per part, so a part has 24 at least, and
+// there are at most four.
+struct RoundShare {
+  int me, n, kb, whole, parts, cut_tiles, at;
+  bool part_left;               // this pair's part of a cut tile is still to come
+
+  __device__ __forceinline__ RoundShare(int me_, int n_, int n_tiles, int kb_, bool may_cut)
+      : me(me_), n(n_), kb(kb_), whole(n_tiles), parts(1), cut_tiles(0), at(me_) {
+    const int rest = n_tiles % n;
+    if (may_cut && rest > 0) {
+      parts = min(min(n / rest, kb / 24), 4);
+      if (parts > 1) {
+        cut_tiles = rest;
+        whole = n_tiles - rest;
+      }
+    }
+    part_left = me < cut_tiles * parts;
+  }
+  __device__ __forceinline__ bool next(Piece& c) {
+    if (at < whole) {
+      c.tile = at;
+      c.kb0 = 0;
+      c.kb1 = kb;
+      at += n;
+      return true;
+    }
+    if (!part_left) return false;
+    part_left = false;
+    const int q = me / parts, r = me - q * parts;
+    c.tile = whole + q;
+    c.kb0 = kb * r / parts;
+    c.kb1 = kb * (r + 1) / parts;
+    return true;
+  }
+  __device__ __forceinline__ bool cut(const Piece& c) const { return c.tile >= whole; }
+  __device__ __forceinline__ void owners(int t, int& first, int& last) const {
+    first = (t - whole) * parts;
+    last = first + parts - 1;
   }
 };
 
@@ -298,6 +329,15 @@ __device__ __forceinline__ bool arrive_last(int* header, int counter, int n, Epi
   return last;
 }
 
+// (a0, a1) += (b0 c0, b1 c1), one instruction for both.
+__device__ __forceinline__ void fma2(float& a0, float& a1, float b0, float b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\t"
+      "fma.rn.f32x2 a, b, c, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
 // ------------------------------------------------------------------ stream kernel
 template <bool F8, int OP>
 struct StreamCfg {
@@ -368,7 +408,7 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Schedule sched(blockIdx.x, gridDim.x, n_tiles, 0, p.k_blocks, 2);
+  EvenShare sched(blockIdx.x, gridDim.x, n_tiles, p.k_blocks);
   Piece c;
 
   if (warp == 0) {
@@ -634,6 +674,12 @@ __device__ __forceinline__ int half_cols(int rows, int h) {
   return m > 0 ? (m + 31) & ~31 : 0;
 }
 
+// Whether K block kb of a TN tile ends inside a 16-row step of the MMA.
+__device__ __forceinline__ bool ragged_block(int rows, int kb) {
+  const int left = rows - kb * 64;
+  return left < 64 && (left & 15) != 0;
+}
+
 template <bool F8, int OP, typename OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kThreads, 1)
     pair_kernel(const __grid_constant__ ProductArgs p) {
@@ -662,7 +708,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(&full_bar[i], OP == kTN ? 2 : 1);
+      mbar_init(&full_bar[i], OP == kTN ? 2 : 1);     // TN: see the producer
       mbar_init(&empty_bar[i], 1);
       mbar_init(&land_bar[i], 1);
     }
@@ -692,12 +738,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
-  // K blocks of a tile (TN: of the only group, where tiles may be cut), and the tiles of the
-  // last round, whose K blocks are shared out if that round would leave pairs idle
+  // K blocks of a tile (TN: of the only group; with several, tiles differ and are not cut)
   const int kb_all = OP == kTN ? (n_tiles ? (gt.off[1] - gt.off[0] + 63) / 64 : 1) : p.k_blocks;
-  const int rest = n_tiles % n_pairs;
-  const bool share = (OP != kTN || p.n_groups == 1) && kb_all >= 8 && rest * 10 < n_pairs * 9;
-  Schedule sched(pair, n_pairs, n_tiles, share ? n_tiles - rest : n_tiles, kb_all, 4);
+  RoundShare sched(pair, n_pairs, n_tiles, kb_all, OP != kTN || p.n_groups == 1);
   // The next piece of work and its tile; a whole TN tile has its own group's K blocks.
   Piece c;
   Tile t;
@@ -730,14 +773,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
           uint8_t* st = tiles + stage * C::kStage;
           uint8_t* bt = st + kTileA;
           if (OP == kTN) {
+            // loads count on the leader's barrier, which the leader's producer arrives on
+            // twice; those of a ragged last block count on this CTA's own, and the CTAs'
+            // zeroing warps arrive on the leader's, once each, when its rows are in order
             const int half = grad_n() / 2;                        // columns per CTA: 64 or 128
             const int y = t.row0 + kb * 64;
-            uint64_t* bar = &land_bar[stage];
-            mbar_arrive_expect_tx(bar, kTileA + half * 128);
-            tma_load_2d(st, &p.wmap, bar, m0, y);
-            tma_load_2d(st + kBox, &p.wmap, bar, m0 + 64, y);
+            const bool ragged = ragged_block(t.rows, kb);
+            const uint32_t bytes = kTileA + half * 128;
+            const uint32_t bar = mapa_shared(ragged ? &land_bar[stage] : &full_bar[stage], ragged ? rank : 0);
+            if (ragged) {
+              mbar_arrive_expect_tx(&land_bar[stage], bytes);
+            } else if (leader) {
+              mbar_arrive(&full_bar[stage]);
+              mbar_arrive_expect_tx(&full_bar[stage], 2 * bytes);
+            }
+            tma_load_2d_pair(st, &p.wmap, bar, m0, y);
+            tma_load_2d_pair(st + kBox, &p.wmap, bar, m0 + 64, y);
             for (int x = 0; x < half; x += 64)
-              tma_load_2d(bt + x * 128, &p.tmap[0], bar, t.nb * 256 + rank * half + x, y);
+              tma_load_2d_pair(bt + x * 128, &p.tmap[0], bar, t.nb * 256 + rank * half + x, y);
           } else {
             const uint32_t bar = mapa_shared(&full_bar[stage], 0);
             const int kx = kb * (F8 ? 128 : 64);
@@ -873,36 +926,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
     } else if (OP == kTN) {
       // -------------------------------------------------------- rows behind the group's last
       // The last K block's rows past the group belong to the next group (or to nobody): in both
-      // operands they are overwritten with zeros up to the MMA's 16-row step.  Then this CTA's
-      // half of the stage is ready: the leader's barrier counts both.
+      // operands they are overwritten with zeros up to the MMA's 16-row step.
       int stage = 0;
-      uint32_t phase = 0;
+      uint32_t parity = 0;                       // bit s: phase of land_bar[s]
       bool ok = true;
       while (ok && fetch()) {
         const int boxes = 2 + grad_n() / 128;
-        for (int kb = c.kb0; kb < c.kb1; ++kb) {
-          const bool w = mbar_wait(&land_bar[stage], phase, abort_flag, status);
+        for (int kb = c.kb0; kb < c.kb1; ++kb, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
+          if (!ragged_block(t.rows, kb)) continue;
+          const bool w = mbar_wait(&land_bar[stage], (parity >> stage) & 1u, abort_flag, status);
           if (!__all_sync(0xffffffffu, w)) {
             ok = false;
             break;
           }
+          parity ^= 1u << stage;
           const int left = t.rows - kb * 64;
-          if (left < 64 && (left & 15)) {
-            uint8_t* st = tiles + stage * C::kStage;
-            const int units = (16 - (left & 15)) * 8;             // 16-byte pieces per box
-            for (int i = lane; i < units * boxes; i += 32) {
-              const int box = i / units;
-              *reinterpret_cast<uint4*>(st + box * kBox + left * 128 + (i - box * units) * 16) =
-                  make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
+          uint8_t* st = tiles + stage * C::kStage;
+          const int units = (16 - (left & 15)) * 8;               // 16-byte pieces per box
+          for (int i = lane; i < units * boxes; i += 32) {
+            const int box = i / units;
+            *reinterpret_cast<uint4*>(st + box * kBox + left * 128 + (i - box * units) * 16) =
+                make_uint4(0, 0, 0, 0);
           }
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(&full_bar[stage], 0));
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
       }
     }
@@ -927,8 +975,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
       int first = 0, last = 0;
       if (cut) sched.owners(c.tile, first, last);
       auto slot = [&](int owner) {
-        return p.partials +
-               ((static_cast<size_t>(owner) * 2 + (owner == first ? 1 : 0)) * 2 + rank) * (128 * 256) + m_local;
+        return p.partials + (static_cast<size_t>(owner) * 2 + rank) * (128 * 256) + m_local;
       };
       // sixteen columns of the finished tile to global memory
       auto finish = [&](const float (&v)[16], int n0) {
@@ -976,15 +1023,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
             tc_fence_after();
             const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols + part * 64;
 #pragma unroll
-            for (int q = 0; q < 4; q += 2) {
-              if (h * 128 + part * 64 + q * 16 < t.rows) {
-                float v0[16], v1[16];
-                tmem_ld16x2(tb + q * 16, tb + q * 16 + 16, v0, v1);
+            for (int q = 0; q < 4; ++q) {
+              if (h * 128 + part * 64 + q * 16 >= t.rows) break;
+              float v[16];
+              tmem_ld16(tb + q * 16, v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  acc[h][q][i] = fmaf(sc[h * 128 + q * 16 + i], v0[i], acc[h][q][i]);
-                  acc[h][q + 1][i] = fmaf(sc[h * 128 + q * 16 + 16 + i], v1[i], acc[h][q + 1][i]);
-                }
+              for (int i = 0; i < 16; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(sc + h * 128 + q * 16 + i);
+                fma2(acc[h][q][i], acc[h][q][i + 1], f.x, f.y, v[i], v[i + 1]);
+                fma2(acc[h][q][i + 2], acc[h][q][i + 3], f.z, f.w, v[i + 2], v[i + 3]);
               }
             }
             release(b);
@@ -1030,10 +1077,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
         float v[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = 0.f;
-        for (int owner = first; owner <= last; ++owner) {
-          const float* from = slot(owner);
+        for (int owner = first; owner <= last; owner += 2) {      // two parts' loads in flight
+          const float* a = slot(owner) + n0 * 128;
+          const float* b = slot(min(owner + 1, last)) + n0 * 128;
+          float x[16], y[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += __ldcg(from + (n0 + i) * 128);
+          for (int i = 0; i < 16; ++i) {
+            x[i] = __ldcg(a + i * 128);
+            y[i] = owner < last ? __ldcg(b + i * 128) : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = (v[i] + x[i]) + y[i];
         }
         finish(v, n0);
         if (F8 && (n0 & 63) == 48) n0 += 64;     // the other warps' 64 columns
@@ -1053,7 +1107,7 @@ static_assert(kStreamCtas <= kMaxCounters && 2 * kPairs <= kMaxCounters, "join c
 
 size_t product_workspace() {
   const size_t stream = sizeof(float) * 2 * kStreamCtas * StreamCfg<true, kNT>::kTileFloats;
-  const size_t pair = sizeof(float) * 2 * kPairs * PairCfg<false, kNT>::kTileFloats;
+  const size_t pair = sizeof(float) * kPairs * PairCfg<false, kNT>::kTileFloats;
   return kProductHeader + (stream > pair ? stream : pair);
 }
 
