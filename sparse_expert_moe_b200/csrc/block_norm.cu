@@ -25,8 +25,6 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxThreads = 1024;
-
 struct NormArgs {
   const void *r, *y, *w_post, *gate, *w_pre;
   void *r_out, *h;
@@ -39,40 +37,43 @@ struct NormArgs {
   float inv_d, eps, res_scale, branch_scale, w_offset;
 };
 
-// Eight consecutive elements (vector `v`) of a bf16 or fp32 array.
-template <bool F32>
-__device__ __forceinline__ void load8(const void* base, size_t v, float (&f)[8]) {
-  if (F32) {
-    const float4* p = static_cast<const float4*>(base) + 2 * v;
-    const float4 a = p[0], b = p[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  } else {
-    const uint4 q = static_cast<const uint4*>(base)[v];
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+// Eight consecutive elements as four pairs.
+struct Vec8 {
+  float2 p[4];
+};
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ Vec8 constant8(float v) {
+  return Vec8{{both(v), both(v), both(v), both(v)}};
+}
+__device__ __forceinline__ Vec8 unpack_bf16(const uint4& a) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  Vec8 f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
+  for (int i = 0; i < 4; ++i)
+    f.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  return f;
 }
-__device__ __forceinline__ void load8(const void* base, size_t v, bool f32, float (&f)[8]) {
-  if (f32) load8<true>(base, v, f);
-  else load8<false>(base, v, f);
+__device__ __forceinline__ Vec8 unpack_f32(const uint4& a, const uint4& b) {
+  return Vec8{{make_float2(__uint_as_float(a.x), __uint_as_float(a.y)),
+               make_float2(__uint_as_float(a.z), __uint_as_float(a.w)),
+               make_float2(__uint_as_float(b.x), __uint_as_float(b.y)),
+               make_float2(__uint_as_float(b.z), __uint_as_float(b.w))}};
 }
-
-template <bool F32>
-__device__ __forceinline__ void store8(void* base, size_t v, const float (&f)[8]) {
-  if (F32) {
-    float4* p = static_cast<float4*>(base) + 2 * v;
-    p[0] = make_float4(f[0], f[1], f[2], f[3]);
-    p[1] = make_float4(f[4], f[5], f[6], f[7]);
+// Vector `v` (elements 8 v .. 8 v + 7) of a bf16 or fp32 array.
+__device__ __forceinline__ Vec8 load8(const void* base, size_t v, bool f32) {
+  const uint4* q = static_cast<const uint4*>(base);
+  return f32 ? unpack_f32(q[2 * v], q[2 * v + 1]) : unpack_bf16(q[v]);
+}
+__device__ __forceinline__ void store8(void* base, size_t v, bool f32, const Vec8& f) {
+  if (f32) {
+    float4* o = static_cast<float4*>(base) + 2 * v;
+    o[0] = make_float4(f.p[0].x, f.p[0].y, f.p[1].x, f.p[1].y);
+    o[1] = make_float4(f.p[2].x, f.p[2].y, f.p[3].x, f.p[3].y);
   } else {
     uint4 q;
     __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&q);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(f.p[i].x, f.p[i].y);
     static_cast<uint4*>(base)[v] = q;
   }
 }
@@ -108,16 +109,16 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* part, int tpr) {
 }
 
 // Rows on their way in: each thread copies the vectors that it alone will read into its own
-// places of shared memory with cp.async, kStages - 1 rows ahead, so a CTA keeps that many rows
-// in flight without holding them in registers and without a barrier (a thread waits for its own
+// places of shared memory with cp.async, kStages - 1 rows ahead of the one it finishes, so a CTA
+// keeps rows in flight without holding them in registers and without a barrier (a thread waits for its own
 // copies).  kStages = 0: rows are read from global memory directly (few rows per CTA).
 template <int kStages>
-__device__ __forceinline__ void rows_wait() {
-  if (kStages) asm volatile("cp.async.wait_group %0;" ::"n"(kStages ? kStages - 1 : 0) : "memory");
+__device__ __forceinline__ void rows_wait() {   // all but the newest kStages - 2 rows
+  if (kStages) asm volatile("cp.async.wait_group %0;" ::"n"(kStages ? kStages - 2 : 0) : "memory");
 }
 __device__ __forceinline__ void rows_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// One array's vectors of a thread in one stage: VPT x (16 or 32 bytes), thread-interleaved.
+// One array's vectors of a thread in one stage: 16 or 32 bytes each, thread-interleaved.
 template <bool F32>
 __device__ __forceinline__ void stage_in(uint4* st, int slot, int threads, const void* base, size_t v) {
   const uint4* g = static_cast<const uint4*>(base);
@@ -128,49 +129,37 @@ __device__ __forceinline__ void stage_in(uint4* st, int slot, int threads, const
     cp_async_16_cg(st + slot * threads, g + v);
   }
 }
-template <bool F32>
-__device__ __forceinline__ void unpack8(const uint4& a, const uint4& b, float (&f)[8]) {
-  if (F32) {
-    f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
-    f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
-    f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
-    f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
-  } else {
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(w[i] << 16);
-      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  }
-}
 // Vector `slot` of this thread: from its stage, or straight from the array.
 template <bool F32, bool STAGED>
-__device__ __forceinline__ void row8(const uint4* st, int slot, int threads, const void* base, size_t v,
-                                     float (&f)[8]) {
-  if (STAGED) {
-    const uint4 a = st[(F32 ? 2 * slot : slot) * threads];
-    unpack8<F32>(a, F32 ? st[(2 * slot + 1) * threads] : a, f);
-  } else {
-    load8<F32>(base, v, f);
-  }
+__device__ __forceinline__ Vec8 row8(const uint4* st, int slot, int threads, const void* base, size_t v) {
+  if (!STAGED) return load8(base, v, F32);
+  if (F32) return unpack_f32(st[2 * slot * threads], st[(2 * slot + 1) * threads]);
+  return unpack_bf16(st[slot * threads]);
 }
 
 // Thread i of a row holds vectors i, i + tpr, ...; a CTA walks rows blockIdx.x * rows + row,
-// + gridDim.x * rows, ...  Measured at T = 8192, d = 7168, bf16, post-norm, token gate and
-// pre-norm (470 MB): one row per CTA without staging 172 us (2.7 TB/s: the loads of a row and
-// its two sums take turns).
+// + gridDim.x * rows, ...  What multiplies a channel in every row is fetched and combined once,
+// into registers: c = branch_scale (w_post + o) (channel gate), and w_pre + o.
+//
+// Bound by HBM where rows are many.  Measured at T = 8192, d = 7168, bf16, post-norm, token gate
+// and pre-norm (470 MB): one row per CTA, scalar arithmetic, weights fetched per row 172 us
+// (2.7 TB/s); staged 134 us, with 50 instructions per element issued 57% of the time; the
+// present form is given at its launch.
 template <bool RES32, bool ACT32, int VPT, int kStages>
-__global__ void __launch_bounds__(VPT == 4 ? 512 : kMaxThreads) block_norm_kernel(const NormArgs p) {
-  __shared__ float part[2][32];
+__global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 448 : 512),
+                                  kStages > 0 && VPT == 2 ? 2 : 1)
+    block_norm_kernel(const NormArgs p) {
+  __shared__ float part[2][64];
   extern __shared__ uint4 ring[];
   constexpr bool kStaged = kStages > 0;
-  constexpr int kR = RES32 ? 2 : 1, kY = ACT32 ? 2 : 1;
+  constexpr int kRing = kStaged ? kStages : 1;
+  constexpr int kAtY = VPT * (RES32 ? 2 : 1), kAtGate = kAtY + VPT * (ACT32 ? 2 : 1);
   const int threads = blockDim.x;
   const int row = threadIdx.x / p.tpr, i0 = threadIdx.x - row * p.tpr;
   const int step = gridDim.x * p.rows;
   const bool full_gate = p.gate_kind == MOE_GATE_FULL;
-  const int stage_vecs = VPT * (kR + (p.y ? kY : 0) + (full_gate ? kY : 0)) * threads;
+  const int stage_vecs =
+      (p.y ? kAtGate + (full_gate ? VPT * (ACT32 ? 2 : 1) : 0) : kAtY) * threads;
   auto fetch = [&](int t, int s) {
     if (t < p.T) {
       uint4* st = ring + s * stage_vecs + threadIdx.x;
@@ -180,8 +169,8 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : kMaxThreads) block_norm_kerne
         const int v = i0 + j * p.tpr;
         if (v >= p.nvec) break;
         stage_in<RES32>(st, j, threads, p.r, base + v);
-        if (p.y) stage_in<ACT32>(st + VPT * kR * threads, j, threads, p.y, base + v);
-        if (full_gate) stage_in<ACT32>(st + VPT * (kR + kY) * threads, j, threads, p.gate, base + v);
+        if (p.y) stage_in<ACT32>(st + kAtY * threads, j, threads, p.y, base + v);
+        if (full_gate) stage_in<ACT32>(st + kAtGate * threads, j, threads, p.gate, base + v);
       }
     }
     rows_commit();
@@ -189,104 +178,159 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : kMaxThreads) block_norm_kerne
   if (kStaged)
     for (int s = 0; s + 1 < kStages; ++s) fetch(blockIdx.x * p.rows + row + s * step, s);
 
-  int turn = 0;
-  // every thread of the CTA makes the same number of turns (row_sums synchronises it)
-  for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, ++turn) {
-    const int t = t0 + row;
-    const bool live = t < p.T;
-    const size_t base = static_cast<size_t>(live ? t : 0) * p.nvec;
-    const uint4* st = nullptr;
-    if (kStaged) {
-      fetch(t + (kStages - 1) * step, (turn + kStages - 1) % (kStaged ? kStages : 1));
-      rows_wait<kStages>();
-      st = ring + turn % (kStaged ? kStages : 1) * stage_vecs + threadIdx.x;
-    }
-    float r[VPT][8], u[VPT][8];
-    float ss[1] = {0.f};
+  Vec8 c[VPT], w[VPT];
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int v = i0 + j * p.tpr;
-      if (live && v < p.nvec) {
-        row8<RES32, kStaged>(st, j, threads, p.r, base + v, r[j]);
-        if (p.y) row8<ACT32, kStaged>(st + VPT * kR * threads, j, threads, p.y, base + v, u[j]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[j][e] = u[j][e] = 0.f;
-      }
-    }
+  for (int j = 0; j < VPT; ++j) {
+    const int v = i0 + j * p.tpr;
+    c[j] = constant8(p.branch_scale);
+    w[j] = constant8(0.f);
+    if (v >= p.nvec) continue;
     if (p.w_post) {
+      const Vec8 a = load8(p.w_post, v, p.w_f32);
 #pragma unroll
-      for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss[0] = fmaf(u[j][e], u[j][e], ss[0]);
-      row_sums(ss, part[0], p.tpr);
+      for (int e = 0; e < 4; ++e)
+        c[j].p[e] = mul2(c[j].p[e], make_float2(a.p[e].x + p.w_offset, a.p[e].y + p.w_offset));
     }
-    const float i_y = rsqrtf(fmaf(ss[0], p.inv_d, p.eps));
-    float tok = p.branch_scale;
-    if (p.gate_kind == MOE_GATE_TOKEN && live) tok *= load1(p.gate, t, p.w_f32);
-    ss[0] = 0.f;
+    if (p.gate_kind == MOE_GATE_CHANNEL) {
+      const Vec8 a = load8(p.gate, v, p.w_f32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[j].p[e] = mul2(c[j].p[e], a.p[e]);
+    }
+    if (p.w_pre) {
+      w[j] = load8(p.w_pre, v, p.w_f32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[j].p[e] = make_float2(w[j].p[e].x + p.w_offset, w[j].p[e].y + p.w_offset);
+    }
+  }
+
+  Vec8 r[VPT];
+  // A: this thread's part of the sum of y^2 of row t
+  auto branch_square = [&](int t, const uint4* st) {
+    float2 s2 = both(0.f);
+    const size_t base = static_cast<size_t>(t) * p.nvec;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (!live || v >= p.nvec) continue;
-      float c[8];
-      if (p.y) {
-        if (p.w_post) {
-          load8(p.w_post, v, p.w_f32, c);
+      if (t >= p.T || v >= p.nvec) continue;
+      const Vec8 y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[j][e] *= i_y * (c[e] + p.w_offset);
-        }
-        if (p.gate_kind == MOE_GATE_CHANNEL || full_gate) {
-          if (full_gate) row8<ACT32, kStaged>(st + VPT * (kR + kY) * threads, j, threads, p.gate, base + v, c);
-          else load8(p.gate, v, p.w_f32, c);
+      for (int e = 0; e < 4; ++e) s2 = fma2(y.p[e], y.p[e], s2);
+    }
+    return s2.x + s2.y;
+  };
+  // B: r' of row t into r and out, and this thread's part of the sum of its squares
+  auto residual = [&](int t, const uint4* st, float tok) {       // tok = i_y (token gate)
+    float2 s2 = both(0.f);
+    if (t >= p.T) return 0.f;
+    const size_t base = static_cast<size_t>(t) * p.nvec;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) u[j][e] *= c[e];
-        }
+    for (int j = 0; j < VPT; ++j) {
+      const int v = i0 + j * p.tpr;
+      if (v >= p.nvec) continue;
+      if (kStaged) r[j] = row8<RES32, kStaged>(st, j, threads, p.r, base + v);
+      if (p.res_scale != 1.f) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r[j][e] = fmaf(tok, u[j][e], p.res_scale * r[j][e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[j][e] *= p.res_scale;
+        for (int e = 0; e < 4; ++e) r[j].p[e] = mul2(both(p.res_scale), r[j].p[e]);
       }
-      if (p.r_out) store8<RES32>(p.r_out, base + v, r[j]);
+      if (p.y) {
+        Vec8 y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
+        if (full_gate) {
+          const Vec8 g = row8<ACT32, kStaged>(st + kAtGate * threads, j, threads, p.gate, base + v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss[0] = fmaf(r[j][e], r[j][e], ss[0]);
+          for (int e = 0; e < 4; ++e) y.p[e] = mul2(y.p[e], g.p[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) r[j].p[e] = fma2(mul2(both(tok), y.p[e]), c[j].p[e], r[j].p[e]);
+      }
+      if (p.r_out) store8(p.r_out, base + v, RES32, r[j]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s2 = fma2(r[j].p[e], r[j].p[e], s2);
     }
-    if (!p.w_pre) {                            // (uniform over the grid)
-      __syncthreads();                         // part[0] is free for the next row
-      continue;
-    }
-    row_sums(ss, part[1], p.tpr);
-    const float i_r = rsqrtf(fmaf(ss[0], p.inv_d, p.eps));
+    return s2.x + s2.y;
+  };
+  // C: h of row t from r
+  auto normalised = [&](int t, float ss) {
+    if (t >= p.T) return;
+    const size_t base = static_cast<size_t>(t) * p.nvec;
+    const float2 i_r = both(rsqrtf(fmaf(ss, p.inv_d, p.eps)));
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (!live || v >= p.nvec) continue;      // for e4m3: whole half-warps at a time
-      float c[8];
-      load8(p.w_pre, v, p.w_f32, c);
+      if (v >= p.nvec) continue;               // for e4m3: whole half-warps at a time
+      Vec8 h;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) c[e] = r[j][e] * i_r * (c[e] + p.w_offset);
-      if (p.out == MOE_BF16) {
-        store8<false>(p.h, base + v, c);
-      } else if (p.out == MOE_F32) {
-        store8<true>(p.h, base + v, c);
+      for (int e = 0; e < 4; ++e) h.p[e] = mul2(mul2(r[j].p[e], i_r), w[j].p[e]);
+      if (p.out != MOE_E4M3) {
+        store8(p.h, base + v, p.out == MOE_F32, h);
       } else {
         // 16 consecutive threads (a half-warp: tpr is a multiple of 32) hold a 128-value block
         uint32_t amax = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(fabsf(c[e])));
+        for (int e = 0; e < 4; ++e)
+          amax = max(amax, max(__float_as_uint(fabsf(h.p[e].x)), __float_as_uint(fabsf(h.p[e].y))));
         amax = __reduce_max_sync((threadIdx.x & 16) ? 0xFFFF0000u : 0x0000FFFFu, amax);
         const int ex = e4m3_scale_exponent(amax);
         uint2 q;
         uint16_t* qh = reinterpret_cast<uint16_t*>(&q);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          qh[e] = __nv_cvt_float2_to_fp8x2(make_float2(scalbnf(c[2 * e], -ex), scalbnf(c[2 * e + 1], -ex)),
+          qh[e] = __nv_cvt_float2_to_fp8x2(make_float2(scalbnf(h.p[e].x, -ex), scalbnf(h.p[e].y, -ex)),
                                            __NV_SATFINITE, __NV_E4M3);
         static_cast<uint2*>(p.h)[base + v] = q;
         if ((v & 15) == 0) p.h_scale[(base + v) >> 4] = ldexpf(1.0f, ex);
       }
     }
+  };
+  auto i_of = [&](float ss) { return p.w_post ? rsqrtf(fmaf(ss, p.inv_d, p.eps)) : 1.f; };
+  auto token_gate = [&](int t) {
+    return p.gate_kind == MOE_GATE_TOKEN && t < p.T ? load1(p.gate, t, p.w_f32) : 1.f;
+  };
+
+  if (!kStaged) {                              // one row per row slot
+    const int t = blockIdx.x * p.rows + row;
+    if (t < p.T) {                             // the loads of r before the sum over y
+#pragma unroll
+      for (int j = 0; j < VPT; ++j)
+        if (i0 + j * p.tpr < p.nvec) r[j] = load8(p.r, static_cast<size_t>(t) * p.nvec + i0 + j * p.tpr, RES32);
+    }
+    const float g = token_gate(t);
+    float sy[1] = {0.f};
+    if (p.w_post) {
+      sy[0] = branch_square(t, nullptr);
+      row_sums(sy, part[0], p.tpr);
+    }
+    float sr[1] = {residual(t, nullptr, i_of(sy[0]) * g)};
+    if (!p.w_pre) return;
+    row_sums(sr, part[1], p.tpr);
+    normalised(t, sr[0]);
+    return;
+  }
+  // Staged: B of row t and A of the next row share one pass to the row's sums, so a turn meets
+  // one barrier and has the work of two rows around it.  Every thread of the CTA makes the same
+  // number of turns.
+  int t = blockIdx.x * p.rows + row;
+  rows_wait<kStages>();                        // the first row (kStages - 1 are under way)
+  float sums[2] = {0.f, p.w_post ? branch_square(t, ring + threadIdx.x) : 0.f};
+  if (p.w_post) row_sums(sums, part[1], p.tpr);
+  int turn = 0;
+  float g = token_gate(t);
+  for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, t += step, ++turn) {
+    const float g_next = token_gate(t + step);
+    fetch(t + (kStages - 1) * step, (turn + kStages - 1) % kRing);
+    rows_wait<kStages>();                      // row t + step
+    const uint4* st = ring + turn % kRing * stage_vecs + threadIdx.x;
+    const uint4* next = ring + (turn + 1) % kRing * stage_vecs + threadIdx.x;
+    sums[0] = residual(t, st, i_of(sums[1]) * g);
+    g = g_next;
+    if (p.w_post) {
+      sums[1] = branch_square(t + step, next);
+      row_sums(sums, part[turn & 1], p.tpr);
+    } else if (p.w_pre) {
+      float one[1] = {sums[0]};
+      row_sums(one, part[turn & 1], p.tpr);
+      sums[0] = one[0];
+    }
+    if (p.w_pre) normalised(t, sums[0]);
   }
 }
 
@@ -294,9 +338,9 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : kMaxThreads) block_norm_kerne
 struct NormGradArgs {
   const void *rp, *y, *w_post, *gate, *w_pre, *dh, *dr_out;
   void *dr, *dy, *dgate;
-  float* parts;                   // [3][n_parts][d]: dw_pre, dw_post, channel dgate
+  float* parts;                   // [2][n_parts][d]: sums for dw_pre, and for dw_post / channel dgate
   int n_parts;
-  bool want_pre, want_post, want_gate;
+  bool want_pre, want_branch, want_gate;
   int T, d, nvec, tpr, rows;
   int gate_kind;
   bool w_f32;
@@ -304,36 +348,38 @@ struct NormGradArgs {
 };
 
 // Rows as in the forward kernel, read again from the stage (or from L1 / L2) in each of the
-// three passes over a row, so that between its two sums only one value per element lives in
-// registers.  A thread keeps the column sums of its own vectors over its rows in registers
-// (VPT <= 2) or in its own places of shared memory, and writes them at the end as one partial
-// per row slot.
+// three passes over a row, so that between its sums only one value per element lives in
+// registers.  Two sums over tokens per channel are enough for all three channel gradients:
+//   A = sum_t dh r' i_r                 dw_pre
+//   B = sum_t b g_t G y i_y             dw_post = B (channel gate),  dgate = B (w_post + o)
+// (g_t the token or full gate, 1 with a channel gate, which is constant over tokens).  A thread
+// keeps those of its own vectors in registers (VPT <= 2) or in its own places of shared memory,
+// and writes them at the end as one partial per row slot.
 template <bool RES32, bool ACT32, int VPT, int kStages>
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGradArgs p) {
   constexpr bool kSmem = VPT > 2, kStaged = kStages > 0;
   static_assert(!(kSmem && kStaged), "shared memory holds the column sums or the stages");
+  constexpr int kRing = kStaged ? kStages : 1;
   constexpr int kR = RES32 ? 2 : 1, kY = ACT32 ? 2 : 1;
-  __shared__ float part[2][16 * 3];
-  extern __shared__ uint4 ring[];              // kSmem: fp32 column sums [3][d]
-  float* acc_smem = reinterpret_cast<float*>(ring);
+  __shared__ float part[2][16 * 5];
+  extern __shared__ uint4 ring[];              // kSmem: fp32 column sums [2][d]
+  float4* sums = reinterpret_cast<float4*>(ring);
   const int threads = blockDim.x;
   const int row = threadIdx.x / p.tpr, i0 = threadIdx.x - row * p.tpr;
   const int step = gridDim.x * p.rows;
-  float acc[kSmem ? 1 : 3][kSmem ? 1 : VPT][8];
+  Vec8 A[kSmem ? 1 : VPT], B[kSmem ? 1 : VPT];
   if (kSmem) {
-    for (int i = threadIdx.x; i < 3 * p.d; i += threads) acc_smem[i] = 0.f;
+    for (int i = threadIdx.x; i < p.d / 2; i += threads) sums[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     __syncthreads();
   } else {
 #pragma unroll
-    for (int a = 0; a < 3; ++a)
-#pragma unroll
-      for (int j = 0; j < VPT; ++j)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[kSmem ? 0 : a][kSmem ? 0 : j][e] = 0.f;
+    for (int j = 0; j < VPT; ++j) A[kSmem ? 0 : j] = B[kSmem ? 0 : j] = constant8(0.f);
   }
-  auto add = [&](int a, int j, int v, int e, float x) {
-    if (kSmem) acc_smem[a * p.d + v * 8 + e] += x;
-    else acc[kSmem ? 0 : a][kSmem ? 0 : j][e] += x;
+  auto smem_add = [&](int which, int v, const Vec8& x) {
+    float4* s = sums + which * (p.d / 4) + 2 * v;
+    const float4 a = s[0], b = s[1];
+    s[0] = make_float4(a.x + x.p[0].x, a.y + x.p[0].y, a.z + x.p[1].x, a.w + x.p[1].y);
+    s[1] = make_float4(b.x + x.p[2].x, b.y + x.p[2].y, b.z + x.p[3].x, b.w + x.p[3].y);
   };
   // stage: r' and dh (with the pre-norm), dr_out, y, full gate -- in fixed places
   constexpr int kAtDh = VPT * kR, kAtDr = kAtDh + VPT * kY, kAtY = kAtDr + VPT * kR, kAtGate = kAtY + VPT * kY;
@@ -361,155 +407,238 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
   if (kStaged)
     for (int s = 0; s + 1 < kStages; ++s) fetch(blockIdx.x * p.rows + row + s * step, s);
 
-  int turn = 0;
-  // every thread of the CTA makes the same number of turns (row_sums synchronises it)
-  for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, ++turn) {
-    const int t = t0 + row;
-    const bool live = t < p.T;
-    const size_t base = static_cast<size_t>(live ? t : 0) * p.nvec;
-    const uint4* st = nullptr;
-    if (kStaged) {
-      fetch(t + (kStages - 1) * step, (turn + kStages - 1) % (kStaged ? kStages : 1));
-      rows_wait<kStages>();
-      st = ring + turn % (kStaged ? kStages : 1) * stage_vecs + threadIdx.x;
+  // w_pre + o, and c = (w_post + o) (channel gate): in registers unless a thread has too many
+  auto pre_weight = [&](int v) {
+    Vec8 a = load8(p.w_pre, v, p.w_f32);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) a.p[e] = make_float2(a.p[e].x + p.w_offset, a.p[e].y + p.w_offset);
+    return a;
+  };
+  auto branch_weight = [&](int v) {
+    Vec8 a = constant8(1.f);
+    if (p.w_post) {
+      a = load8(p.w_post, v, p.w_f32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a.p[e] = make_float2(a.p[e].x + p.w_offset, a.p[e].y + p.w_offset);
     }
-    float x[8], y[8], z[8], c[8];
-    float s[3] = {0.f, 0.f, 0.f};              // r'^2, z r', y^2
+    if (p.gate_kind == MOE_GATE_CHANNEL) {
+      const Vec8 g = load8(p.gate, v, p.w_f32);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a.p[e] = mul2(a.p[e], g.p[e]);
+    }
+    return a;
+  };
+  Vec8 w[kSmem ? 1 : VPT], c[kSmem ? 1 : VPT];
+  if (!kSmem) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (!live || v >= p.nvec) continue;
-      if (p.w_pre) {
-        row8<RES32, kStaged>(st, j, threads, p.rp, base + v, x);
-        row8<ACT32, kStaged>(st + kAtDh * threads, j, threads, p.dh, base + v, z);
-        load8(p.w_pre, v, p.w_f32, c);
+      w[kSmem ? 0 : j] = c[kSmem ? 0 : j] = constant8(0.f);
+      if (v >= p.nvec) continue;
+      if (p.w_pre) w[kSmem ? 0 : j] = pre_weight(v);
+      c[kSmem ? 0 : j] = branch_weight(v);
+    }
+  }
+
+  Vec8 q[VPT];
+  // 1: this thread's parts of the sums of r'^2, z r' and y^2 of row t
+  auto squares = [&](int t, const uint4* st, float* s) {
+    float2 s0 = both(0.f), s1 = both(0.f), s2 = both(0.f);
+    const size_t base = static_cast<size_t>(t) * p.nvec;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s[0] = fmaf(x[e], x[e], s[0]);
-          s[1] = fmaf(z[e] * (c[e] + p.w_offset), x[e], s[1]);
+    for (int j = 0; j < VPT; ++j) {
+      const int v = i0 + j * p.tpr;
+      if (t >= p.T || v >= p.nvec) continue;
+      if (p.w_pre) {
+        const Vec8 x = row8<RES32, kStaged>(st, j, threads, p.rp, base + v);
+        const Vec8 z = row8<ACT32, kStaged>(st + kAtDh * threads, j, threads, p.dh, base + v);
+        const Vec8 wj = kSmem ? pre_weight(v) : w[kSmem ? 0 : j];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s0 = fma2(x.p[e], x.p[e], s0);
+          s1 = fma2(mul2(z.p[e], wj.p[e]), x.p[e], s1);
         }
       }
       if (p.w_post) {
-        row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v, y);
+        const Vec8 y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[2] = fmaf(y[e], y[e], s[2]);
+        for (int e = 0; e < 4; ++e) s2 = fma2(y.p[e], y.p[e], s2);
       }
     }
-    row_sums(s, part[0], p.tpr);
-    const float i_r = rsqrtf(fmaf(s[0], p.inv_d, p.eps));
-    const float k_r = i_r * i_r * i_r * (s[1] * p.inv_d);
-    const float i_y = p.w_post ? rsqrtf(fmaf(s[2], p.inv_d, p.eps)) : 1.f;
-    float tok = p.branch_scale;
-    if (p.gate_kind == MOE_GATE_TOKEN && live) tok *= load1(p.gate, t, p.w_f32);
-    float m[2] = {0.f, 0.f};                   // q y, G u
-    float q[VPT][8];
+    s[0] = s0.x + s0.y;
+    s[1] = s1.x + s1.y;
+    s[2] = s2.x + s2.y;
+  };
+  // 2: G of row t (dr, the channel sums), q kept, and the parts of the sums of q y and G u
+  auto gradients = [&](int t, const uint4* st, float tok, float i_r, float zr, float i_y, float* m) {
+    m[0] = m[1] = 0.f;
+    if (t >= p.T) return;
+    const size_t base = static_cast<size_t>(t) * p.nvec;
+    const float2 k_r = both(-i_r * i_r * i_r * (zr * p.inv_d));
+    float2 m0 = both(0.f), m1 = both(0.f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
+      if (v >= p.nvec) continue;
+      Vec8 G = constant8(0.f);
+      if (p.dr_out) G = row8<RES32, kStaged>(st + kAtDr * threads, j, threads, p.dr_out, base + v);
+      if (p.w_pre) {
+        const Vec8 x = row8<RES32, kStaged>(st, j, threads, p.rp, base + v);
+        const Vec8 z = row8<ACT32, kStaged>(st + kAtDh * threads, j, threads, p.dh, base + v);
+        const Vec8 wj = kSmem ? pre_weight(v) : w[kSmem ? 0 : j];
+        Vec8 zx;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[j][e] = 0.f;
-      if (!live || v >= p.nvec) continue;
-      float G[8];
-      if (p.dr_out) {
-        row8<RES32, kStaged>(st + kAtDr * threads, j, threads, p.dr_out, base + v, G);
+        for (int e = 0; e < 4; ++e) {
+          const float2 zi = mul2(z.p[e], both(i_r));
+          if (!kSmem) A[kSmem ? 0 : j].p[e] = fma2(zi, x.p[e], A[kSmem ? 0 : j].p[e]);
+          else zx.p[e] = mul2(zi, x.p[e]);
+          G.p[e] = fma2(zi, wj.p[e], fma2(k_r, x.p[e], G.p[e]));
+        }
+        if (kSmem && p.want_pre) smem_add(0, v, zx);
+      }
+      Vec8 y = constant8(0.f), g = constant8(1.f);
+      if (p.y) y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
+      if (full_gate) g = row8<ACT32, kStaged>(st + kAtGate * threads, j, threads, p.gate, base + v);
+      if (p.res_scale != 1.f) {
+        Vec8 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o.p[e] = mul2(both(p.res_scale), G.p[e]);
+        store8(p.dr, base + v, RES32, o);
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) G[e] = 0.f;
+        store8(p.dr, base + v, RES32, G);
       }
-      if (p.w_pre) {
-        row8<RES32, kStaged>(st, j, threads, p.rp, base + v, x);
-        row8<ACT32, kStaged>(st + kAtDh * threads, j, threads, p.dh, base + v, z);
-        load8(p.w_pre, v, p.w_f32, c);
+      if (!p.y) continue;
+      const Vec8 cj = kSmem ? branch_weight(v) : c[kSmem ? 0 : j];
+      Vec8 b;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          G[e] += i_r * z[e] * (c[e] + p.w_offset) - k_r * x[e];
-          if (p.want_pre) add(0, j, v, e, z[e] * (x[e] * i_r));
+      for (int e = 0; e < 4; ++e) {
+        const float2 n = mul2(y.p[e], both(i_y));                // normalised branch
+        float2 dn = mul2(both(tok), G.p[e]);
+        if (full_gate) dn = mul2(dn, g.p[e]);
+        q[j].p[e] = mul2(dn, cj.p[e]);                           // q (dy itself without w_post)
+        m0 = fma2(q[j].p[e], y.p[e], m0);
+        if (!kSmem) B[kSmem ? 0 : j].p[e] = fma2(dn, n, B[kSmem ? 0 : j].p[e]);
+        else b.p[e] = mul2(dn, n);
+      }
+      if (kSmem && p.want_branch) smem_add(1, v, b);
+      if (p.want_gate && p.gate_kind != MOE_GATE_CHANNEL) {
+        Vec8 dg;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 u = mul2(mul2(both(p.branch_scale), cj.p[e]), mul2(y.p[e], both(i_y)));
+          dg.p[e] = mul2(G.p[e], u);
+          m1 = fma2(G.p[e], u, m1);
         }
+        if (full_gate) store8(p.dgate, base + v, ACT32, dg);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = p.res_scale * G[e];
-      if (!p.y) {
-        store8<RES32>(p.dr, base + v, x);
-        continue;
-      }
-      row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v, y);
-      if (full_gate) row8<ACT32, kStaged>(st + kAtGate * threads, j, threads, p.gate, base + v, z);
-      store8<RES32>(p.dr, base + v, x);
-      if (p.gate_kind == MOE_GATE_CHANNEL) load8(p.gate, v, p.w_f32, z);
-      if (p.w_post) load8(p.w_post, v, p.w_f32, c);
-      float dg[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float w = p.w_post ? c[e] + p.w_offset : 1.f;
-        const float n = y[e] * i_y;                               // normalised branch
-        const float bg = p.gate_kind == MOE_GATE_CHANNEL || full_gate ? tok * z[e] : tok;
-        const float dn = bg * G[e];                               // gradient of norm(y; w_post)
-        dg[e] = p.branch_scale * G[e] * (n * w);
-        m[1] += dg[e];
-        if (p.want_post) add(1, j, v, e, dn * n);
-        if (p.want_gate && p.gate_kind == MOE_GATE_CHANNEL) add(2, j, v, e, dg[e]);
-        q[j][e] = dn * w;                                         // dy itself without w_post
-        m[0] = fmaf(q[j][e], y[e], m[0]);
-      }
-      if (p.want_gate && full_gate) store8<ACT32>(p.dgate, base + v, dg);
     }
-    if (!p.y) {                                // (uniform over the grid)
-      __syncthreads();                         // part[0] is free for the next row
-      continue;
-    }
-    row_sums(m, part[1], p.tpr);
-    const float k_y = i_y * i_y * i_y * (m[0] * p.inv_d);
-    if (live && i0 == 0 && p.want_gate && p.gate_kind == MOE_GATE_TOKEN)
-      static_cast<float*>(p.dgate)[t] = m[1];
+    m[0] = m0.x + m0.y;
+    m[1] = m1.x + m1.y;
+  };
+  // 3: dy of row t
+  auto branch_gradient = [&](int t, const uint4* st, float i_y, float qy, float gu) {
+    if (t >= p.T || !p.y) return;
+    const size_t base = static_cast<size_t>(t) * p.nvec;
+    const float2 k_y = both(-i_y * i_y * i_y * (qy * p.inv_d));
+    if (i0 == 0 && p.want_gate && p.gate_kind == MOE_GATE_TOKEN) static_cast<float*>(p.dgate)[t] = gu;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (!live || v >= p.nvec) continue;
+      if (v >= p.nvec) continue;
       if (p.w_post) {
-        row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v, y);
+        const Vec8 y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q[j][e] = i_y * q[j][e] - k_y * y[e];
+        for (int e = 0; e < 4; ++e) q[j].p[e] = fma2(both(i_y), q[j].p[e], mul2(k_y, y.p[e]));
       }
-      store8<ACT32>(p.dy, base + v, q[j]);
+      store8(p.dy, base + v, ACT32, q[j]);
+    }
+  };
+  auto i_of = [&](float ss) { return rsqrtf(fmaf(ss, p.inv_d, p.eps)); };
+  auto scale_of = [&](int t) {                 // branch_scale (token gate)
+    return p.gate_kind == MOE_GATE_TOKEN && t < p.T ? p.branch_scale * load1(p.gate, t, p.w_f32) : p.branch_scale;
+  };
+
+  int t = blockIdx.x * p.rows + row;
+  if (!kStaged) {
+    // every thread of the CTA makes the same number of turns (row_sums synchronises it)
+    for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, t += step) {
+      float s[3], m[2];
+      squares(t, nullptr, s);
+      row_sums(s, part[0], p.tpr);
+      const float i_y = p.w_post ? i_of(s[2]) : 1.f;
+      gradients(t, nullptr, scale_of(t), i_of(s[0]), s[1], i_y, m);
+      row_sums(m, part[1], p.tpr);
+      branch_gradient(t, nullptr, i_y, m[0], m[1]);
+    }
+  } else {
+    // 2 of row t and 1 of the next row share one pass to the row's sums (see the forward kernel)
+    rows_wait<kStages>();
+    float s[5];                                // row t + step: 0..2; row t: 3, 4
+    {
+      float f[3];
+      squares(t, ring + threadIdx.x, f);
+      row_sums(f, part[1], p.tpr);
+      s[0] = f[0];
+      s[1] = f[1];
+      s[2] = f[2];
+    }
+    int turn = 0;
+    float tok = scale_of(t);
+    for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, t += step, ++turn) {
+      const float tok_next = scale_of(t + step);
+      fetch(t + (kStages - 1) * step, (turn + kStages - 1) % kRing);
+      rows_wait<kStages>();                    // row t + step
+      const uint4* st = ring + turn % kRing * stage_vecs + threadIdx.x;
+      const float i_y = p.w_post ? i_of(s[2]) : 1.f;
+      gradients(t, st, tok, i_of(s[0]), s[1], i_y, s + 3);
+      tok = tok_next;
+      squares(t + step, ring + (turn + 1) % kRing * stage_vecs + threadIdx.x, s);
+      row_sums(s, part[turn & 1], p.tpr);
+      branch_gradient(t, st, i_y, s[3], s[4]);
     }
   }
   const size_t slot = static_cast<size_t>(blockIdx.x) * p.rows + row;
 #pragma unroll
-  for (int a = 0; a < 3; ++a) {
-    if (!(a == 0 ? p.want_pre : (a == 1 ? p.want_post : p.want_gate && p.gate_kind == MOE_GATE_CHANNEL)))
-      continue;
+  for (int a = 0; a < 2; ++a) {
+    if (!(a == 0 ? p.want_pre : p.want_branch)) continue;
     float* out = p.parts + (static_cast<size_t>(a) * p.n_parts + slot) * p.d;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
       if (v >= p.nvec) continue;
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        f[e] = kSmem ? acc_smem[a * p.d + v * 8 + e] : acc[kSmem ? 0 : a][kSmem ? 0 : j][e];
-      store8<true>(out, v, f);
+      Vec8 f;
+      if (kSmem) f = load8(sums + a * (p.d / 4), v, true);
+      else f = a == 0 ? A[kSmem ? 0 : j] : B[kSmem ? 0 : j];
+      store8(out, v, true, f);
     }
   }
 }
 
-// Column sums of up to three [n_parts][d] arrays: a CTA takes 32 columns of one of them, its
-// 8 warps every 8th partial, joined in a fixed order.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float* __restrict__ parts, int n_parts,
-                                                        int d, float* o0, float* o1, float* o2) {
+// Sums of the partials: a CTA takes 32 channels of A (blockIdx.y = 0) or B (1), its 8 warps
+// every 8th partial, joined in a fixed order; B gives dw_post and the channel gate's gradient.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const NormGradArgs p, float* dw_pre, float* dw_post,
+                                                        float* dgate) {
   __shared__ float s[8][33];
-  float* out = blockIdx.y == 0 ? o0 : (blockIdx.y == 1 ? o1 : o2);
-  if (!out) return;
+  const bool branch = blockIdx.y != 0;
+  if (branch ? !p.want_branch : !p.want_pre) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
-  const float* src = parts + static_cast<size_t>(blockIdx.y) * n_parts * d;
+  const float* src = p.parts + static_cast<size_t>(blockIdx.y) * p.n_parts * p.d;
   float v = 0.f;
-  if (col < d)
-    for (int i = w; i < n_parts; i += 8) v += src[static_cast<size_t>(i) * d + col];
+  if (col < p.d)
+#pragma unroll 8
+    for (int i = w; i < p.n_parts; i += 8) v += src[static_cast<size_t>(i) * p.d + col];
   s[w][lane] = v;
   __syncthreads();
-  if (w == 0 && col < d) {
+  if (w == 0 && col < p.d) {
     for (int i = 1; i < 8; ++i) v += s[i][lane];
-    out[col] = v;
+    if (!branch) {
+      dw_pre[col] = v;
+    } else {
+      const bool channel = p.gate_kind == MOE_GATE_CHANNEL;
+      if (dw_post) dw_post[col] = channel ? v * load1(p.gate, col, p.w_f32) : v;
+      if (dgate) dgate[col] = p.w_post ? v * (load1(p.w_post, col, p.w_f32) + p.w_offset) : v;
+    }
   }
 }
 
@@ -519,13 +648,13 @@ constexpr int kBackwardCtas = 148;             // partial sums per row slot: one
 struct BackwardShape {
   int vpt, tpr, rows;
 };
-// Threads hold one vector of 8 (two above 512 threads, four above 1024); short rows share a CTA.
+// Threads hold two vectors of 8 (one up to 32 of them, four above 1024); short rows share a CTA.
 BackwardShape backward_shape(int d) {
   const int nvec = d / 8;
   BackwardShape s;
-  s.vpt = nvec <= 512 ? 1 : (nvec <= 1024 ? 2 : 4);
+  s.vpt = nvec <= 32 ? 1 : (nvec <= 1024 ? 2 : 4);
   s.tpr = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
-  s.rows = s.tpr >= 256 ? 1 : 256 / s.tpr;
+  s.rows = 512 / s.tpr;
   return s;
 }
 
@@ -545,7 +674,7 @@ moe_status check_norm(const moe_norm_config* c) {
 
 size_t backward_workspace(const moe_norm_config& c) {
   const BackwardShape s = backward_shape(c.d_model);
-  return kNormHeader + sizeof(float) * 3 * static_cast<size_t>(kBackwardCtas) * s.rows * c.d_model;
+  return kNormHeader + sizeof(float) * 2 * static_cast<size_t>(kBackwardCtas) * s.rows * c.d_model;
 }
 
 bool unaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
@@ -559,15 +688,15 @@ template <bool RES32, bool ACT32, int VPT>
 cudaError_t launch_forward_typed(const NormArgs& a, cudaStream_t s) {
   const int64_t turns = (static_cast<int64_t>(a.T) + a.rows - 1) / a.rows;
   const int threads = a.tpr * a.rows;
-  if constexpr (VPT == 4) {
+  if constexpr (VPT > 1) {
     // staged: three rows in flight per CTA, as many CTAs per SM as their stages leave room for
-    // (at most four), if every CTA then gets at least three rows
+    // (at most eight), if every CTA then gets at least three rows
     constexpr int kStages = 3;
     const size_t smem = static_cast<size_t>(kStages) * VPT * threads * 16 *
                         ((RES32 ? 2 : 1) + ((a.y != nullptr) + (a.gate_kind == MOE_GATE_FULL)) * (ACT32 ? 2 : 1));
     int ctas = static_cast<int>(kSmemPerSm / (smem + 1024));
-    if (ctas > 4) ctas = 4;
-    if (ctas >= 1 && turns >= 3 * kSms * ctas) {
+    if (ctas > 8) ctas = 8;
+    if (ctas >= 1 && turns >= 3 * kSms * ctas && threads <= (VPT == 2 ? 448 : 512)) {
       const cudaError_t e = cudaFuncSetAttribute(block_norm_kernel<RES32, ACT32, VPT, kStages>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  static_cast<int>(smem));
@@ -603,7 +732,7 @@ cudaError_t launch_backward_typed(const NormGradArgs& a, unsigned grid, cudaStre
       return cudaGetLastError();
     }
   }
-  const size_t smem = VPT > 2 ? sizeof(float) * 3 * a.d : 0;
+  const size_t smem = VPT > 2 ? sizeof(float) * 2 * a.d : 0;
   if (smem) {
     const cudaError_t e = cudaFuncSetAttribute(block_norm_backward_kernel<RES32, ACT32, VPT, 0>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -663,7 +792,7 @@ moe_status moe_block_norm(const moe_norm_config* cfg, const void* r, const void*
   a.w_offset = cfg->w_offset;
   // few tokens: as many threads per row as it has vectors, for the shortest chain; many: four
   // vectors per thread, which keeps more loads in flight per thread and more CTAs on an SM
-  const int vpt = a.nvec > 2048 ? 4 : (cfg->T <= 296 ? (a.nvec <= 1024 ? 1 : 2) : (a.nvec <= 64 ? 1 : 4));
+  const int vpt = a.nvec > 2048 ? 4 : (cfg->T <= 296 ? (a.nvec <= 1024 ? 1 : 2) : (a.nvec <= 64 ? 1 : (a.nvec <= 896 ? 2 : 4)));
   a.tpr = ((a.nvec + vpt - 1) / vpt + 31) / 32 * 32;
   a.rows = a.tpr >= 128 ? 1 : 128 / a.tpr;
   const bool res32 = cfg->res == MOE_F32, act32 = cfg->act == MOE_F32;
@@ -695,8 +824,8 @@ moe_status moe_block_norm_backward(const moe_norm_config* cfg, const void* r_out
   a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + kNormHeader);
   a.n_parts = static_cast<int>(grid) * sh.rows;
   a.want_pre = dw_pre != nullptr;
-  a.want_post = dw_post != nullptr;
   a.want_gate = dgate != nullptr;
+  a.want_branch = dw_post || (dgate && cfg->gate == MOE_GATE_CHANNEL);
   a.T = cfg->T;
   a.d = cfg->d_model;
   a.nvec = cfg->d_model / 8;
@@ -717,9 +846,8 @@ moe_status moe_block_norm_backward(const moe_norm_config* cfg, const void* r_out
     if (e != cudaSuccess) return MOE_ERR_CUDA;
   }
   float* dgc = cfg->gate == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
-  if (dw_pre || dw_post || dgc) {
-    sum_parts_kernel<<<dim3((a.d + 31) / 32, 3), 256, 0, stream>>>(a.parts, a.n_parts, a.d, dw_pre, dw_post,
-                                                                    dgc);
+  if (a.want_pre || a.want_branch) {
+    sum_parts_kernel<<<dim3((a.d + 31) / 32, 2), 256, 0, stream>>>(a, dw_pre, dw_post, dgc);
     return ok_or_cuda(cudaGetLastError());
   }
   return MOE_OK;

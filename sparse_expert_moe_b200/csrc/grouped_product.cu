@@ -329,15 +329,6 @@ __device__ __forceinline__ bool arrive_last(int* header, int counter, int n, Epi
   return last;
 }
 
-// (a0, a1) += (b0 c0, b1 c1), one instruction for both.
-__device__ __forceinline__ void fma2(float& a0, float& a1, float b0, float b1, float c0, float c1) {
-  asm("{\n\t.reg .b64 a, b, c;\n\t"
-      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\t"
-      "fma.rn.f32x2 a, b, c, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(a0), "+f"(a1)
-      : "f"(b0), "f"(b1), "f"(c0), "f"(c1));
-}
-
 // ------------------------------------------------------------------ stream kernel
 template <bool F8, int OP>
 struct StreamCfg {
@@ -1030,8 +1021,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
 #pragma unroll
               for (int i = 0; i < 16; i += 4) {
                 const float4 f = *reinterpret_cast<const float4*>(sc + h * 128 + q * 16 + i);
-                fma2(acc[h][q][i], acc[h][q][i + 1], f.x, f.y, v[i], v[i + 1]);
-                fma2(acc[h][q][i + 2], acc[h][q][i + 3], f.z, f.w, v[i + 2], v[i + 3]);
+                float2* a = reinterpret_cast<float2*>(&acc[h][q][i]);
+                a[0] = fma2(make_float2(f.x, f.y), make_float2(v[i], v[i + 1]), a[0]);
+                a[1] = fma2(make_float2(f.z, f.w), make_float2(v[i + 2], v[i + 3]), a[1]);
               }
             }
             release(b);

@@ -34,6 +34,25 @@ __device__ __forceinline__ int e4m3_scale_exponent(uint32_t amax_bits) {
   return max(-127, min(127, e));
 }
 
+// ---------------------------------------------------------------- packed fp32
+// Two fp32 operations per instruction, each rounded as its scalar form.
+__device__ __forceinline__ unsigned long long bits2(float2 a) {
+  return static_cast<unsigned long long>(__float_as_uint(a.y)) << 32 | __float_as_uint(a.x);
+}
+__device__ __forceinline__ float2 from_bits2(unsigned long long v) {
+  return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return from_bits2(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return from_bits2(d);
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
