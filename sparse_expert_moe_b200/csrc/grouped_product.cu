@@ -1203,8 +1203,9 @@ moe_status moe_grouped_gemm(const moe_product_config* cfg, const int32_t* group_
   if (cfg->n_rows == 0) return MOE_OK;
   if (!a || !w || !y || (f8 && (!a_scale || !w_scale))) return MOE_ERR_INVALID_ARG;
   ProductArgs p = product_args(*cfg, group_offsets, y, ws);
+  const bool few = few_rows(*cfg);
   bool ok = make_tmap_matrix(&p.wmap, w, f8, cfg->n_groups, cfg->n, cfg->k, 128);
-  for (int i = 0; i < 4 && ok; ++i)
+  for (int i = few ? 2 : 0; i < 4 && ok; ++i)    // the stream kernel takes boxes of 32 and 16 rows
     ok = f8 ? make_tmap_u8(&p.tmap[i], a, cfg->n_rows, cfg->k, 128u >> i)
             : make_tmap_bf16(&p.tmap[i], a, cfg->n_rows, cfg->k, 128u >> i);
   if (!ok) return MOE_ERR_CUDA;
@@ -1214,8 +1215,7 @@ moe_status moe_grouped_gemm(const moe_product_config* cfg, const int32_t* group_
   p.w_scale = w_scale;
   p.w_scale_rows = (cfg->n + 127) / 128;
   const bool f32 = cfg->out == MOE_F32;
-  return f8 ? launch_product<true, kNT>(p, f32, few_rows(*cfg), stream)
-            : launch_product<false, kNT>(p, f32, few_rows(*cfg), stream);
+  return f8 ? launch_product<true, kNT>(p, f32, few, stream) : launch_product<false, kNT>(p, f32, few, stream);
 }
 
 moe_status moe_grouped_gemm_dgrad(const moe_product_config* cfg, const int32_t* group_offsets, const void* dy,
@@ -1226,12 +1226,13 @@ moe_status moe_grouped_gemm_dgrad(const moe_product_config* cfg, const int32_t* 
   if (cfg->n_rows == 0) return MOE_OK;
   if (!dy || !w || !da) return MOE_ERR_INVALID_ARG;
   ProductArgs p = product_args(*cfg, group_offsets, da, ws);
+  const bool few = few_rows(*cfg);
   bool ok = make_tmap_matrix(&p.wmap, w, false, cfg->n_groups, cfg->n, cfg->k, 64);
-  for (int i = 0; i < 4 && ok; ++i) ok = make_tmap_bf16(&p.tmap[i], dy, cfg->n_rows, cfg->n, 128u >> i);
+  for (int i = few ? 2 : 0; i < 4 && ok; ++i) ok = make_tmap_bf16(&p.tmap[i], dy, cfg->n_rows, cfg->n, 128u >> i);
   if (!ok) return MOE_ERR_CUDA;
   p.m_total = p.ld_out = cfg->k;
   p.k_blocks = (cfg->n + 63) / 64;
-  return launch_product<false, kNN>(p, cfg->out == MOE_F32, few_rows(*cfg), stream);
+  return launch_product<false, kNN>(p, cfg->out == MOE_F32, few, stream);
 }
 
 moe_status moe_grouped_gemm_wgrad(const moe_product_config* cfg, const int32_t* group_offsets, const void* dy,

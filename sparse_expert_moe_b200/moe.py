@@ -275,55 +275,51 @@ def moe_status_string(code: int) -> str:
 _VALUE_TYPES = {0: torch.float32, 1: torch.bfloat16, 2: torch.float8_e4m3fn, 4: torch.float8_e4m3fn}
 
 
-class _Args:
-    """Checks the tensors of one call (type, size, contiguous, one device) on their way to
-    pointers, and finds the device and stream the call runs on.  Plain integers pass as
-    device addresses."""
+def _device_of(*tensors) -> int:
+    """Index of the CUDA device of the first tensor among them (-1: only addresses)."""
+    for t in tensors:
+        if t is not None and type(t) is not int:
+            return t.get_device() if t.is_cuda else -2
+    return -1
 
-    __slots__ = ("fn", "device")
 
-    def __init__(self, fn: str):
-        self.fn, self.device = fn, -1
-
-    def __call__(self, name: str, t, code: int, numel: int):
-        if t is None or isinstance(t, int):
-            return t
-        want = _VALUE_TYPES.get(code)      # None: a type the library refuses by itself
-        if want is not None and t.dtype is not want and not (code in (2, 4) and t.dtype is torch.uint8):
-            raise TypeError(f"{self.fn}: {name} is {t.dtype}, not {want}")
-        return self.raw(name, t, numel)
-
-    def raw(self, name: str, t, numel: int):
-        if t is None or isinstance(t, int):
-            return t
-        if t.numel() != numel or not t.is_contiguous():
-            raise ValueError(f"{self.fn}: {name} must be contiguous with {numel} elements, got shape "
-                             f"{tuple(t.shape)}, strides {t.stride()}")
-        d = t.get_device()
-        if d != self.device or d < 0:
-            if d < 0 or self.device >= 0:
-                raise ValueError(f"{self.fn}: {name} is not on the CUDA device of the other tensors")
-            self.device = d
+def _addr(fn: str, name: str, t, want, numel: int, device: int):
+    """Device address of a tensor of one call, checked: its type (None: any), element count,
+    contiguity and device.  None and plain integers (device addresses) pass."""
+    if t is None or type(t) is int:
+        return t
+    if (t.dtype is want or want is None) and t.numel() == numel and t.is_contiguous() and \
+            t.get_device() == device:
         return t.data_ptr()
+    if want is torch.float8_e4m3fn and t.dtype is torch.uint8:       # codes as bytes
+        return _addr(fn, name, t, torch.uint8, numel, device)
+    if want is not None and t.dtype is not want:
+        raise TypeError(f"{fn}: {name} is {t.dtype}, not {want}")
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous with {numel} elements, got shape "
+                         f"{tuple(t.shape)}, strides {t.stride()}")
+    raise ValueError(f"{fn}: {name} is not on the CUDA device of the other tensors")
 
-    def offsets(self, t, n_groups: int):
-        if t is not None and not isinstance(t, int) and t.dtype is not torch.int32:
-            raise TypeError(f"{self.fn}: group_offsets is {t.dtype}, not torch.int32")
-        return self.raw("group_offsets", t, n_groups + 1)
 
-    def workspace(self, ws):
-        if isinstance(ws, int) or ws is None:
-            raise TypeError(f"{self.fn}: the workspace is a tensor")
-        return self.raw("ws", ws, ws.numel()), ws.numel() * ws.element_size()
+def _workspace(fn: str, ws, device: int):
+    if ws is None or type(ws) is int:
+        raise TypeError(f"{fn}: the workspace is a tensor")
+    n = ws.numel()
+    return _addr(fn, "ws", ws, None, n, device), n * ws.element_size()
 
-    def run(self, stream, *args):
-        """The C call on the tensors' device, on `stream` or that device's current stream."""
-        fn = getattr(load_library(), self.fn)
-        if self.device < 0 or self.device == torch.cuda.current_device():
-            _check(self.fn, fn(*args, _stream(stream)))
-        else:
-            with torch.cuda.device(self.device):
-                _check(self.fn, fn(*args, _stream(stream)))
+
+def _call(fn: str, device: int, stream, *args):
+    """The C call on the tensors' device, on `stream` or that device's current stream."""
+    f = getattr(_lib or load_library(), fn)
+    if device < 0:
+        code = f(*args, _stream(stream))
+    elif device == torch.cuda.current_device():
+        code = f(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            code = f(*args, _stream(stream))
+    if code != MOE_OK:
+        raise MoeError(fn, code)
 
 
 def make_norm_config(T, d_model, gate="none", res="bf16", act="bf16", weight="bf16", out="bf16", eps=1e-6,
@@ -341,33 +337,41 @@ def moe_norm_workspace_size(cfg: MoeNormConfig) -> int:
 
 def _gate_shape(cfg: MoeNormConfig):
     """(elements, type code) of the gate."""
-    if cfg.gate == GATE["full"]:
+    if cfg.gate == 3:
         return cfg.T * cfg.d_model, cfg.act
-    return (cfg.T if cfg.gate == GATE["token"] else cfg.d_model), cfg.weight
+    return (cfg.T if cfg.gate == 2 else cfg.d_model), cfg.weight
 
 
 def moe_block_norm(cfg: MoeNormConfig, r, y, w_post, gate, w_pre, r_out, h, h_scale, stream=None):
     """r_out = res_scale r + branch_scale gate norm(y; w_post), h = norm(r_out; w_pre); see
     include/moe.h for what may be None."""
-    a = _Args("moe_block_norm")
+    fn, D = "moe_block_norm", _VALUE_TYPES.get
+    dev = _device_of(r, y, w_post, gate, w_pre, r_out, h, h_scale)
     d, n = cfg.d_model, cfg.T * cfg.d_model
+    res, act, wt = D(cfg.res), D(cfg.act), D(cfg.weight)
     gn, gt = _gate_shape(cfg)
-    a.run(stream, ctypes.byref(cfg), a("r", r, cfg.res, n), a("y", y, cfg.act, n),
-          a("w_post", w_post, cfg.weight, d), a("gate", gate, gt, gn), a("w_pre", w_pre, cfg.weight, d),
-          a("r_out", r_out, cfg.res, n), a("h", h, cfg.out, n), a("h_scale", h_scale, 0, n // 128))
+    _call(fn, dev, stream, ctypes.byref(cfg), _addr(fn, "r", r, res, n, dev), _addr(fn, "y", y, act, n, dev),
+          _addr(fn, "w_post", w_post, wt, d, dev), _addr(fn, "gate", gate, D(gt), gn, dev),
+          _addr(fn, "w_pre", w_pre, wt, d, dev), _addr(fn, "r_out", r_out, res, n, dev),
+          _addr(fn, "h", h, D(cfg.out), n, dev), _addr(fn, "h_scale", h_scale, torch.float32, n // 128, dev))
 
 
 def moe_block_norm_backward(cfg: MoeNormConfig, r_out, y, w_post, gate, w_pre, dh, dr_out, dr, dy, dgate,
                             dw_post, dw_pre, ws, stream=None):
     """Gradients of moe_block_norm (dr, dy and, where not None, dgate, dw_post, dw_pre)."""
-    a = _Args("moe_block_norm_backward")
+    fn, D, f32 = "moe_block_norm_backward", _VALUE_TYPES.get, torch.float32
+    dev = _device_of(r_out, y, w_post, gate, w_pre, dh, dr_out, dr, dy, dgate, dw_post, dw_pre, ws)
     d, n = cfg.d_model, cfg.T * cfg.d_model
+    res, act, wt = D(cfg.res), D(cfg.act), D(cfg.weight)
     gn, gt = _gate_shape(cfg)
-    a.run(stream, ctypes.byref(cfg), a("r_out", r_out, cfg.res, n), a("y", y, cfg.act, n),
-          a("w_post", w_post, cfg.weight, d), a("gate", gate, gt, gn), a("w_pre", w_pre, cfg.weight, d),
-          a("dh", dh, cfg.act, n), a("dr_out", dr_out, cfg.res, n), a("dr", dr, cfg.res, n),
-          a("dy", dy, cfg.act, n), a("dgate", dgate, gt if cfg.gate == GATE["full"] else 0, gn),
-          a("dw_post", dw_post, 0, d), a("dw_pre", dw_pre, 0, d), *a.workspace(ws))
+    _call(fn, dev, stream, ctypes.byref(cfg), _addr(fn, "r_out", r_out, res, n, dev),
+          _addr(fn, "y", y, act, n, dev), _addr(fn, "w_post", w_post, wt, d, dev),
+          _addr(fn, "gate", gate, D(gt), gn, dev), _addr(fn, "w_pre", w_pre, wt, d, dev),
+          _addr(fn, "dh", dh, act, n, dev), _addr(fn, "dr_out", dr_out, res, n, dev),
+          _addr(fn, "dr", dr, res, n, dev), _addr(fn, "dy", dy, act, n, dev),
+          _addr(fn, "dgate", dgate, act if cfg.gate == 3 else f32, gn, dev),
+          _addr(fn, "dw_post", dw_post, f32, d, dev), _addr(fn, "dw_pre", dw_pre, f32, d, dev),
+          *_workspace(fn, ws, dev))
 
 
 def make_product_config(n_groups, n_rows, n, k, dtype="bf16", out="bf16") -> MoeProductConfig:
@@ -383,28 +387,37 @@ def moe_product_workspace_size(cfg: MoeProductConfig) -> int:
 
 def moe_grouped_gemm(cfg: MoeProductConfig, group_offsets, a, a_scale, w, w_scale, y, ws, stream=None):
     """y[r] = a[r] W_g^T for the rows r of group g (bf16, or e4m3 with block scales)."""
-    c = _Args("moe_grouped_gemm")
-    G, R, n, k = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k
-    kb, nb = (k + 127) // 128, (n + 127) // 128
-    c.run(stream, ctypes.byref(cfg), c.offsets(group_offsets, G), c("a", a, cfg.in_, R * k),
-          c("a_scale", a_scale, 0, R * kb), c("w", w, cfg.in_, G * n * k),
-          c("w_scale", w_scale, 0, G * nb * kb), c("y", y, cfg.out, R * n), *c.workspace(ws))
+    fn, f32 = "moe_grouped_gemm", torch.float32
+    dev = _device_of(a, w, y, group_offsets, a_scale, w_scale, ws)
+    G, R, n, k, vt = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k, _VALUE_TYPES.get(cfg.in_)
+    kb = (k + 127) // 128
+    _call(fn, dev, stream, ctypes.byref(cfg),
+          _addr(fn, "group_offsets", group_offsets, torch.int32, G + 1, dev), _addr(fn, "a", a, vt, R * k, dev),
+          _addr(fn, "a_scale", a_scale, f32, R * kb, dev), _addr(fn, "w", w, vt, G * n * k, dev),
+          _addr(fn, "w_scale", w_scale, f32, G * ((n + 127) // 128) * kb, dev),
+          _addr(fn, "y", y, _VALUE_TYPES.get(cfg.out), R * n, dev), *_workspace(fn, ws, dev))
 
 
 def moe_grouped_gemm_dgrad(cfg: MoeProductConfig, group_offsets, dy, w, da, ws, stream=None):
     """da[r] = dy[r] W_g: the gradient of moe_grouped_gemm's rows."""
-    c = _Args("moe_grouped_gemm_dgrad")
-    G, R, n, k = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k
-    c.run(stream, ctypes.byref(cfg), c.offsets(group_offsets, G), c("dy", dy, cfg.in_, R * n),
-          c("w", w, cfg.in_, G * n * k), c("da", da, cfg.out, R * k), *c.workspace(ws))
+    fn = "moe_grouped_gemm_dgrad"
+    dev = _device_of(dy, w, da, group_offsets, ws)
+    G, R, n, k, vt = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k, _VALUE_TYPES.get(cfg.in_)
+    _call(fn, dev, stream, ctypes.byref(cfg),
+          _addr(fn, "group_offsets", group_offsets, torch.int32, G + 1, dev), _addr(fn, "dy", dy, vt, R * n, dev),
+          _addr(fn, "w", w, vt, G * n * k, dev), _addr(fn, "da", da, _VALUE_TYPES.get(cfg.out), R * k, dev),
+          *_workspace(fn, ws, dev))
 
 
 def moe_grouped_gemm_wgrad(cfg: MoeProductConfig, group_offsets, dy, a, dw, ws, stream=None):
     """dw_g = sum of dy[r]^T a[r] over the rows of group g: the gradient of the weights."""
-    c = _Args("moe_grouped_gemm_wgrad")
-    G, R, n, k = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k
-    c.run(stream, ctypes.byref(cfg), c.offsets(group_offsets, G), c("dy", dy, cfg.in_, R * n),
-          c("a", a, cfg.in_, R * k), c("dw", dw, cfg.out, G * n * k), *c.workspace(ws))
+    fn = "moe_grouped_gemm_wgrad"
+    dev = _device_of(dw, dy, a, group_offsets, ws)
+    G, R, n, k, vt = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k, _VALUE_TYPES.get(cfg.in_)
+    _call(fn, dev, stream, ctypes.byref(cfg),
+          _addr(fn, "group_offsets", group_offsets, torch.int32, G + 1, dev), _addr(fn, "dy", dy, vt, R * n, dev),
+          _addr(fn, "a", a, vt, R * k, dev), _addr(fn, "dw", dw, _VALUE_TYPES.get(cfg.out), G * n * k, dev),
+          *_workspace(fn, ws, dev))
 
 
 # ---------------------------------------------------------------------------
