@@ -232,6 +232,19 @@ bool make_tmap_matrix(CUtensorMap* map, const void* base, bool u8, uint64_t grou
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_store(CUtensorMap* map, void* base, bool f32, uint64_t groups, uint64_t rows, uint64_t cols) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || groups == 0 || rows == 0 || cols == 0) return false;
+  const uint64_t pitch = cols * (f32 ? 4 : 2);
+  const cuuint64_t dims[3] = {cols, rows, groups};
+  const cuuint64_t strides[2] = {pitch, pitch * rows};
+  const cuuint32_t box[3] = {f32 ? 32u : 64u, 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // Token-operand maps with boxes of 128, 64, 32 and 16 rows.

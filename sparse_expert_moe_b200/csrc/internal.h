@@ -167,6 +167,9 @@ bool make_tmap_u8(CUtensorMap* map, const void* base, uint64_t rows, uint64_t co
 // columns give zeros, not the next matrix.  The row pitch must be a multiple of 16 bytes.
 bool make_tmap_matrix(CUtensorMap* map, const void* base, bool u8, uint64_t groups, uint64_t rows,
                       uint64_t cols, uint32_t box_rows);
+// Matrices [groups][rows, cols] of fp32 or bf16 for TMA stores, box {128 bytes of columns,
+// 32 rows, one matrix}, 128-byte swizzle; the row pitch must be a multiple of 16 bytes.
+bool make_tmap_store(CUtensorMap* map, void* base, bool f32, uint64_t groups, uint64_t rows, uint64_t cols);
 // Packed FP4 (two E2M1 codes per byte, `cols` elements per row), box {128 elements,
 // box_rows rows}, loaded into shared memory unpacked to one 16-byte slot per 16 elements
 // (8 data bytes, 8 bytes of gap): the e4m3 tile layout the block-scaled MMA reads FP4
