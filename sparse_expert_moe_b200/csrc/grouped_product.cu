@@ -273,20 +273,24 @@ template <typename T>
 __device__ __forceinline__ void store_transposed(T* out, size_t ld, int rows, int cols, const float* v,
                                                  void* stage_raw, int lane) {
   T* stage = static_cast<T*>(stage_raw);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if constexpr (sizeof(T) == 4) stage[i * 32 + lane] = v[i];
-    else stage[i * 32 + lane] = __float2bfloat16_rn(v[i]);
-  }
-  __syncwarp();
   constexpr int kElems = 16 / static_cast<int>(sizeof(T)), kVecs = 32 / kElems;
+  constexpr int kRun = 1024 / (32 * static_cast<int>(sizeof(T)));  // tokens that fit 1 KB: 16 or 8
 #pragma unroll
-  for (int q = lane; q < 16 * kVecs; q += 32) {
-    const int r = q / kVecs, c = (q % kVecs) * kElems;
-    if (r < rows && c < cols)
-      *reinterpret_cast<uint4*>(out + r * ld + c) = *reinterpret_cast<const uint4*>(stage + r * 32 + c);
+  for (int i0 = 0; i0 < 16; i0 += kRun) {
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      if constexpr (sizeof(T) == 4) stage[i * 32 + lane] = v[i0 + i];
+      else stage[i * 32 + lane] = __float2bfloat16_rn(v[i0 + i]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int q = lane; q < kRun * kVecs; q += 32) {
+      const int r = q / kVecs, c = (q % kVecs) * kElems;
+      if (i0 + r < rows && c < cols)
+        *reinterpret_cast<uint4*>(out + (i0 + r) * ld + c) = *reinterpret_cast<const uint4*>(stage + r * 32 + c);
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 // A warp's 32 rows (lane = row) x 16 columns to rows of `out`, likewise.
 template <typename T>
@@ -430,68 +434,65 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
 
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      while (ok && sched.next(c)) {
-        const Tile t = token_tile(gt, c.tile, C::kNTok, 16, m_blocks, 1);
-        const int box = t.rows > 16 ? 32 : 16;
-        const CUtensorMap* tm = &p.tmap[box == 32 ? 2 : 3];
-        for (int kb = c.kb0; kb < c.kb1; ++kb) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, status)) {
-            ok = false;
-            break;
-          }
-          uint8_t* st = tiles + stage * C::kStage;
-          const int kx = kb * (F8 ? 128 : 64);
-          mbar_arrive_expect_tx(&full_bar[stage], C::kA + box * 128);
+    const bool elected = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    while (ok && sched.next(c)) {
+      const Tile t = token_tile(gt, c.tile, C::kNTok, 16, m_blocks, 1);
+      const int box = t.rows > 16 ? 32 : 16;
+      const CUtensorMap* tm = &p.tmap[box == 32 ? 2 : 3];
+      for (int kb = c.kb0; kb < c.kb1; ++kb) {
+        ok = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
+        if (!ok) break;
+        uint8_t* st = tiles + stage * C::kStage;
+        uint64_t* bar = &full_bar[stage];
+        const int kx = kb * (F8 ? 128 : 64);
+        if (elected) {
+          mbar_arrive_expect_tx(bar, C::kA + box * 128);
           if (OP == kNT) {
 #pragma unroll
             for (int j = 0; j < C::kMB; ++j)
-              tma_load_3d(st + j * kTileA, &p.wmap, &full_bar[stage], kx, (t.mb * C::kMB + j) * 128, t.g);
+              tma_load_3d(st + j * kTileA, &p.wmap, bar, kx, (t.mb * C::kMB + j) * 128, t.g);
           } else {
 #pragma unroll
             for (int j = 0; j < 2 * C::kMB; ++j)
-              tma_load_3d(st + j * kBox, &p.wmap, &full_bar[stage], t.mb * C::kMB * 128 + j * 64, kx, t.g);
+              tma_load_3d(st + j * kBox, &p.wmap, bar, t.mb * C::kMB * 128 + j * 64, kx, t.g);
           }
-          tma_load_2d(st + C::kA, tm, &full_bar[stage], kx, t.row0);
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          tma_load_2d(st + C::kA, tm, bar, kx, t.row0);
+        }
+        __syncwarp();
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
-    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, it = 0;               // accumulator buffers used so far
-      bool ok = true;
-      while (ok && sched.next(c)) {
-        const Tile t = token_tile(gt, c.tile, C::kNTok, 16, m_blocks, 1);
-        const int n_pad = (t.rows + 15) & ~15;
-        const uint32_t idesc = F8 ? idesc_e4m3_f32(128, n_pad)
-                                  : (idesc_bf16_f32(128, n_pad) | (OP == kNN ? kIdescAMajorMN : 0u));
-        uint32_t d0 = 0, b = 0;
-        for (int kb = c.kb0; kb < c.kb1; ++kb) {
-          if (F8 || kb == c.kb0) {              // a fresh accumulator buffer
-            b = it % C::kBufs;
-            if (!mbar_wait(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status)) {
-              ok = false;
-              break;
-            }
-            d0 = tmem + b * C::kCols;
-            ++it;
-          }
-          if (!mbar_wait(&full_bar[stage], phase, abort_flag, status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(tiles) + stage * C::kStage, sb = sa + C::kA;
+    const bool elected = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, it = 0;                 // accumulator buffers used so far
+    bool ok = true;
+    while (ok && sched.next(c)) {
+      const Tile t = token_tile(gt, c.tile, C::kNTok, 16, m_blocks, 1);
+      const int n_pad = (t.rows + 15) & ~15;
+      const uint32_t idesc = F8 ? idesc_e4m3_f32(128, n_pad)
+                                : (idesc_bf16_f32(128, n_pad) | (OP == kNN ? kIdescAMajorMN : 0u));
+      uint32_t d0 = 0, b = 0;
+      for (int kb = c.kb0; kb < c.kb1; ++kb) {
+        if (F8 || kb == c.kb0) {                // a fresh accumulator buffer
+          b = it % C::kBufs;
+          ok = mbar_wait_warp(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status);
+          if (!ok) break;
+          d0 = tmem + b * C::kCols;
+          ++it;
+        }
+        ok = mbar_wait_warp(&full_bar[stage], phase, abort_flag, status);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sa = smem_u32(tiles) + stage * C::kStage, sb = sa + C::kA;
+        if (elected) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t bd = umma_desc_sw128(sb + kk * 32);
@@ -505,16 +506,15 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
             }
           }
           umma_commit(&empty_bar[stage]);
-          if (F8) umma_commit(&tfull_bar[b]);
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (F8 || kb + 1 == c.kb1) umma_commit(&tfull_bar[b]);
         }
-        if (!F8 && ok) umma_commit(&tfull_bar[b]);
+        __syncwarp();
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
-    __syncwarp();
   } else if (warp == 2) {
     // ---------------------------------------------------------- scales (e4m3)
     // For kScaleBlocks K blocks at a time: lane = token fetches its scales, multiplies them by
@@ -664,41 +664,44 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
   if (warp == 1) tmem_dealloc(tmem, C::kTmem);
 }
 
-// ------------------------------------------------------------------ pair kernel
-constexpr size_t kPairPartFloats = 128 * 256;   // a CTA's sums of a cut tile
+constexpr size_t kPairPartFloats = 128 * 256;   // a CTA's fp32 sums of a cut tile, [column][row]
 
-template <bool F8, int OP>
+// Sixteen columns of a cut tile: the sums of its parts, added in order, two parts' loads in flight.
+template <class Slot>
+__device__ __forceinline__ void join_parts(float (&v)[16], Slot slot, int first, int last, int n0) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.f;
+  for (int owner = first; owner <= last; owner += 2) {
+    const float* a = slot(owner) + n0 * 128;
+    const float* b = slot(min(owner + 1, last)) + n0 * 128;
+    float x[16], y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      x[i] = __ldcg(a + i * 128);
+      y[i] = owner < last ? __ldcg(b + i * 128) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = (v[i] + x[i]) + y[i];
+  }
+}
+
+// ------------------------------------------------------------------ pair kernel
+template <int OP>
 struct PairCfg {
   static constexpr int kWidth = 256;                              // tokens (TN: columns) per tile
   static constexpr uint32_t kStage = 2 * kTileA;                  // 128 rows of either operand
-  static constexpr int kStages = F8 || OP == kTN ? 5 : 6;
-  // bf16: two accumulators of 256 columns.  e4m3: a tile's tokens in two halves of up to 128,
-  // two buffers for either, each holding one K block's products: draining one overlaps the
-  // MMAs into the other, and four epilogue warps fold each half.
-  static constexpr int kBufs = F8 ? 4 : 2;
-  static constexpr int kCols = F8 ? 128 : 256;
-  static constexpr int kEpi = F8 ? 8 : 4;                         // epilogue warps
-  static constexpr int kEpi0 = F8 ? 4 : 3;                        // the first of them
+  static constexpr int kStages = OP == kTN ? 5 : 6;
+  static constexpr int kBufs = 2;                                 // accumulators of 256 columns
+  static constexpr int kCols = 256;
+  static constexpr int kEpi = 4, kEpi0 = 3;                       // epilogue warps, the first of them
   static constexpr int kThreads = 32 * (kEpi0 + kEpi);
-  // e4m3: an epilogue thread keeps 128 sums and 32 products: registers move from warps 0..3 to
-  // 4..11.  384 x 168 at launch = 128 x 88 + 256 x 208.
-  static constexpr int kRegsLow = 88, kRegsHigh = 208;
-  static constexpr uint32_t kScales = F8 ? 2 * kScaleBlocks * kWidth * 4 : 0;
   static constexpr uint32_t kWarpStage = OP == kTN ? 2 * 4096 : 2048;
   static constexpr uint32_t kStaging = kEpi * kWarpStage;
            // both CTAs
   static constexpr uint32_t kSmem =
-      1024 + kStages * kStage + 1024 + kScales + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
+      1024 + kStages * kStage + 1024 + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
   static_assert(kSmem <= 227 * 1024, "budget");
 };
-
-// The halves of an e4m3 tile of `rows` tokens: the first holds half_width of them, and both are
-// rounded up so that either CTA of the pair loads a multiple of 16 rows.
-__device__ __forceinline__ int half_width(int rows) { return ((rows + 1) / 2 + 31) & ~31; }
-__device__ __forceinline__ int half_cols(int rows, int h) {
-  const int w = half_width(rows);
-  return h == 0 ? w : (rows > w ? (rows - w + 31) & ~31 : 0);
-}
 
 // Whether K block kb of a TN tile ends inside a 16-row step of the MMA.
 __device__ __forceinline__ bool ragged_block(int rows, int kb) {
@@ -706,10 +709,10 @@ __device__ __forceinline__ bool ragged_block(int rows, int kb) {
   return left < 64 && (left & 15) != 0;
 }
 
-template <bool F8, int OP, typename OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kThreads, 1)
+template <int OP, typename OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThreads, 1)
     pair_kernel(const __grid_constant__ ProductArgs p) {
-  using C = PairCfg<F8, OP>;
+  using C = PairCfg<OP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -718,14 +721,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
   uint64_t* land_bar = empty_bar + C::kStages;        // TN: this CTA's loads of a stage
   uint64_t* tfull_bar = land_bar + C::kStages;
   uint64_t* tempty_bar = tfull_bar + C::kBufs;        // the leader's counts
-  uint64_t* sfull_bar = tempty_bar + C::kBufs;
-  uint64_t* sempty_bar = sfull_bar + 2;
-  uint64_t* epi_bar = sempty_bar + 2;
+  uint64_t* epi_bar = tempty_bar + C::kBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* last_flag = reinterpret_cast<int*>(tmem_slot + 2);
-  float* scales = reinterpret_cast<float*>(tiles + C::kStages * C::kStage + 1024);
-  uint8_t* staging = reinterpret_cast<uint8_t*>(scales) + C::kScales;
+  uint8_t* staging = tiles + C::kStages * C::kStage + 1024;
   GroupTable& gt = *reinterpret_cast<GroupTable*>(staging + C::kStaging);
   int* status = p.header;
 
@@ -740,11 +740,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
     }
     for (int i = 0; i < C::kBufs; ++i) {
       mbar_init(&tfull_bar[i], 1);
-      mbar_init(&tempty_bar[i], 8);                    // four epilogue warps of either CTA
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sfull_bar[i], 1);
-      mbar_init(&sempty_bar[i], C::kEpi);
+      mbar_init(&tempty_bar[i], 2 * C::kEpi);          // both CTAs' epilogue warps
     }
     mbar_init(epi_bar, C::kEpi);
     *abort_flag = 0;
@@ -783,32 +779,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
   auto grad_cols = [&]() { return min(256, p.n_total - t.nb * 256); };
   auto grad_n = [&]() { return grad_cols() > 128 ? 256 : 128; };
 
-  if (warp < C::kEpi0) {
-  if (F8) regs_down<C::kRegsLow>();            // (one instruction for the whole warpgroup)
   if (warp == 0) {
     // ---------------------------------------------------------- TMA producer (both CTAs)
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      while (ok && fetch()) {
-        const int m0 = t.mb * 256 + rank * 128;
-        for (int kb = c.kb0; kb < c.kb1; ++kb) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, status)) {
-            ok = false;
-            break;
-          }
-          uint8_t* st = tiles + stage * C::kStage;
-          uint8_t* bt = st + kTileA;
-          if (OP == kTN) {
-            // loads count on the leader's barrier, which the leader's producer arrives on
-            // twice; those of a ragged last block count on this CTA's own, and the CTAs'
-            // zeroing warps arrive on the leader's, once each, when its rows are in order
-            const int half = grad_n() / 2;                        // columns per CTA: 64 or 128
-            const int y = t.row0 + kb * 64;
-            const bool ragged = ragged_block(t.rows, kb);
-            const uint32_t bytes = kTileA + half * 128;
-            const uint32_t bar = mapa_shared(ragged ? &land_bar[stage] : &full_bar[stage], ragged ? rank : 0);
+    const bool elected = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    while (ok && fetch()) {
+      const int m0 = t.mb * 256 + rank * 128;
+      for (int kb = c.kb0; kb < c.kb1; ++kb) {
+        ok = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
+        if (!ok) break;
+        uint8_t* st = tiles + stage * C::kStage;
+        uint8_t* bt = st + kTileA;
+        if (OP == kTN) {
+          // loads count on the leader's barrier, which the leader's producer arrives on twice;
+          // those of a ragged last block count on this CTA's own, and the CTAs' zeroing warps
+          // arrive on the leader's, once each, when its rows are in order
+          const int half = grad_n() / 2;                          // columns per CTA: 64 or 128
+          const int y = t.row0 + kb * 64, x0 = t.nb * 256 + rank * half;
+          const bool ragged = ragged_block(t.rows, kb);
+          const uint32_t bytes = kTileA + half * 128;
+          const uint32_t bar = mapa_shared(ragged ? &land_bar[stage] : &full_bar[stage], ragged ? rank : 0);
+          if (elected) {
             if (ragged) {
               mbar_arrive_expect_tx(&land_bar[stage], bytes);
             } else if (leader) {
@@ -817,12 +810,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
             }
             tma_load_2d_pair(st, &p.wmap, bar, m0, y);
             tma_load_2d_pair(st + kBox, &p.wmap, bar, m0 + 64, y);
-            for (int x = 0; x < half; x += 64)
-              tma_load_2d_pair(bt + x * 128, &p.tmap[0], bar, t.nb * 256 + rank * half + x, y);
-          } else {
-            const uint32_t bar = mapa_shared(&full_bar[stage], 0);
-            const int kx = kb * (F8 ? 128 : 64);
-            const int n_pad = F8 ? half_cols(t.rows, 0) + half_cols(t.rows, 1) : (t.rows + 31) & ~31;
+            tma_load_2d_pair(bt, &p.tmap[0], bar, x0, y);
+            if (half > 64) tma_load_2d_pair(bt + kBox, &p.tmap[0], bar, x0 + 64, y);
+          }
+        } else {
+          const uint32_t bar = mapa_shared(&full_bar[stage], 0);
+          const int kx = kb * 64;
+          const int n_pad = (t.rows + 31) & ~31;
+          // this CTA's half of the token rows, in boxes of 128, 64, 32 and 16 rows
+          const int rows = n_pad / 2, y = t.row0 + rank * rows;
+          if (elected) {
             if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kTileA + n_pad * 128);
             if (OP == kNT) {
               tma_load_3d_pair(st, &p.wmap, bar, kx, m0, t.g);
@@ -830,131 +827,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
               tma_load_3d_pair(st, &p.wmap, bar, m0, kx, t.g);
               tma_load_3d_pair(st + kBox, &p.wmap, bar, m0 + 64, kx, t.g);
             }
-            // this CTA's half of the token rows (e4m3: of either half tile), in boxes of
-            // 128, 64, 32 and 16 rows
-#pragma unroll
-            for (int h = 0; h < (F8 ? 2 : 1); ++h) {
-              const int rows = (F8 ? half_cols(t.rows, h) : n_pad) / 2;
-              const int y = t.row0 + h * half_width(t.rows) + rank * rows;
-              for (int bi = 0, off = 0; bi < 4; ++bi) {
-                const int box = 128 >> bi;
-                while (rows - off >= box) {
-                  tma_load_2d_pair(bt + h * kBox + off * 128, &p.tmap[bi], bar, kx, y + off);
-                  off += box;
-                }
+            for (int bi = 0, off = 0; bi < 4; ++bi) {
+              const int box = 128 >> bi;
+              while (rows - off >= box) {
+                tma_load_2d_pair(bt + off * 128, &p.tmap[bi], bar, kx, y + off);
+                off += box;
               }
             }
           }
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        __syncwarp();
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
     }
-    __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer (the leader)
-    if (lane == 0 && leader) {
+    if (leader) {
+      const bool elected = elect_one();
       int stage = 0;
-      uint32_t phase = 0, it = 0, it1 = 0;       // e4m3: buffers used by the first, second halves
+      uint32_t phase = 0, it = 0;                // accumulators used so far
       bool ok = true;
       while (ok && fetch()) {
         if (c.kb1 <= c.kb0) continue;                             // TN: a group without rows
-        uint32_t b = 0;
-        if (!F8) {
-          b = it % C::kBufs;
-          if (!mbar_wait(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status)) break;
-          ++it;
-        }
+        const uint32_t b = it % C::kBufs;
+        if (!mbar_wait_warp(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status)) break;
+        ++it;
         const int n_pad = OP == kTN ? grad_n() : (t.rows + 31) & ~31;
         const uint32_t idesc = idesc_bf16_f32(256, n_pad) | (OP != kNT ? kIdescAMajorMN : 0u) |
                                (OP == kTN ? kIdescBMajorMN : 0u);
-        for (int kb = c.kb0; kb < c.kb1 && ok; ++kb) {
+        const uint32_t d = tmem + b * C::kCols;
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
           ok = OP == kTN && ragged_block(t.rows, kb)
-                   ? mbar_wait_cluster(&full_bar[stage], phase, abort_flag, status)
-                   : mbar_wait(&full_bar[stage], phase, abort_flag, status);
+                   ? __all_sync(0xffffffffu, mbar_wait_cluster(&full_bar[stage], phase, abort_flag, status)) != 0
+                   : mbar_wait_warp(&full_bar[stage], phase, abort_flag, status);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sa = smem_u32(tiles) + stage * C::kStage, sb = sa + kTileA;
-          if (F8) {
-            const int halves = half_cols(t.rows, 1) ? 2 : 1;
-            for (int h = 0; h < halves; ++h) {
-              uint32_t& ith = h ? it1 : it;
-              b = 2 * h + (ith & 1);
-              ok = mbar_wait(&tempty_bar[b], ((ith >> 1) & 1u) ^ 1u, abort_flag, status);
-              ++ith;
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t id8 = idesc_e4m3_f32(256, half_cols(t.rows, h));
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_e4m3_pair(tmem + b * C::kCols, umma_desc_sw128(sa + kk * 32),
-                               umma_desc_sw128(sb + h * kBox + kk * 32), id8, kk ? 1u : 0u);
-              if (h + 1 == halves) umma_commit_pair(&empty_bar[stage], 0x3);
-              umma_commit_pair(&tfull_bar[b], 0x3);
-            }
-          } else {
-            const int left = OP == kTN ? t.rows - kb * 64 : 64;
-            const int steps = left < 64 ? (left + 15) / 16 : 4;
-            const uint32_t d = tmem + b * C::kCols;
+          const int left = OP == kTN ? t.rows - kb * 64 : 64;
+          if (elected) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-              if (kk >= steps) break;
+              if (OP == kTN && kk * 16 >= left) break;
               const uint64_t ad = OP == kNT ? umma_desc_sw128(sa + kk * 32) : umma_desc_mn_sw128(sa + kk * 2048);
               const uint64_t bd = OP == kTN ? umma_desc_mn_sw128(sb + kk * 2048) : umma_desc_sw128(sb + kk * 32);
               umma_bf16_pair(d, ad, bd, idesc, (kb > c.kb0 || kk) ? 1u : 0u);
             }
             umma_commit_pair(&empty_bar[stage], 0x3);
+            if (kb + 1 == c.kb1) umma_commit_pair(&tfull_bar[b], 0x3);
           }
+          __syncwarp();
           if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (!F8 && ok) umma_commit_pair(&tfull_bar[b], 0x3);
       }
     }
     __syncwarp();
   } else if (warp == 2) {
-    if (F8) {
-      // -------------------------------------------------------- scales (e4m3, both CTAs)
-      // For kScaleBlocks K blocks at a time: each token's scales times this CTA's weight
-      // block's, as [K block][token].
-      uint32_t it = 0;
-      bool ok = true;
-      while (ok && fetch()) {
-        const float* sw = p.w_scale + (static_cast<size_t>(t.g) * p.w_scale_rows +
-                                       min(2 * t.mb + rank, p.w_scale_rows - 1)) * p.k_blocks;
-        for (int kb = c.kb0; kb < c.kb1; kb += kScaleBlocks, ++it) {
-          const bool w = mbar_wait(&sempty_bar[it & 1], ((it >> 1) & 1u) ^ 1u, abort_flag, status);
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
-          }
-          float* dst = scales + (it & 1) * (kScaleBlocks * C::kWidth);
-          float ws[kScaleBlocks];
-#pragma unroll
-          for (int q = 0; q < kScaleBlocks; ++q) ws[q] = __ldg(sw + min(kb + q, c.kb1 - 1));
-          for (int n0 = 0; n0 < t.rows; n0 += 64) {
-            float s[2][kScaleBlocks];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float* sa = p.a_scale +
-                                static_cast<size_t>(t.row0 + min(n0 + j * 32 + lane, t.rows - 1)) * p.k_blocks;
-#pragma unroll
-              for (int q = 0; q < kScaleBlocks; ++q) s[j][q] = __ldg(sa + min(kb + q, c.kb1 - 1));
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int q = 0; q < kScaleBlocks; ++q) dst[q * C::kWidth + n0 + j * 32 + lane] = s[j][q] * ws[q];
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sfull_bar[it & 1]);
-        }
-      }
-    } else if (OP == kTN) {
+    if (OP == kTN) {
       // -------------------------------------------------------- rows behind the group's last
       // The last K block's rows past the group belong to the next group (or to nobody): in both
       // operands they are overwritten with zeros up to the MMA's 16-row step.
@@ -986,16 +920,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
       }
     }
     __syncwarp();
-  }
   } else {
     // ---------------------------------------------------------- epilogue (both CTAs)
-    if (F8) regs_up<C::kRegsHigh>();
     const int sub = warp & 3;                    // TMEM lane quadrant
-    const int part = (warp - C::kEpi0) >> 2;     // e4m3: half of the tile's tokens
     const int m_local = sub * 32 + lane;
     uint8_t* stg = staging + (warp - C::kEpi0) * C::kWarpStage;
     EpilogueSync sync{epi_bar, abort_flag, status};
-    uint32_t it = 0, sit = 0, stores = 0;
+    uint32_t it = 0, stores = 0;
     bool ok = true;
     auto release = [&](uint32_t b) {
       tc_fence_before();
@@ -1030,55 +961,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
           for (int i = 0; i < 16; ++i) __stcg(mine + (n0 + i) * 128, v[i]);
         }
       };
-      const int h0 = F8 ? part * half_width(t.rows) : 0;          // first token, and tokens, of
-      const int hn = F8 ? min(half_width(t.rows), t.rows - h0) : cols;   // this warp's columns
-      if (F8) {
-        float acc[128];
-#pragma unroll
-        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-        for (int kb = c.kb0; kb < c.kb1; ++kb) {
-          const int kq = (kb - c.kb0) % kScaleBlocks;
-          if (kq == 0) {
-            const bool w = mbar_wait(&sfull_bar[sit & 1], (sit >> 1) & 1u, abort_flag, status);
-            ok = __all_sync(0xffffffffu, w) != 0;
-            if (!ok) break;
-          }
-          if (hn > 0) {
-            const float* sc = scales + ((sit & 1) * kScaleBlocks + kq) * C::kWidth + h0;
-            const uint32_t b = 2 * part + (it & 1);
-            const bool w = mbar_wait(&tfull_bar[b], (it >> 1) & 1u, abort_flag, status);
-            ok = __all_sync(0xffffffffu, w) != 0;
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {        // 32 columns at a time
-              if (q * 32 < hn) {
-                float v[32];
-                tmem_ld32(tb + q * 32, v);
-                if ((q + 1) * 32 >= hn) release(b);
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const float4 f = *reinterpret_cast<const float4*>(sc + q * 32 + i);
-                  float2* a = reinterpret_cast<float2*>(&acc[q * 32 + i]);
-                  a[0] = fma2(make_float2(f.x, f.y), make_float2(v[i], v[i + 1]), a[0]);
-                  a[1] = fma2(make_float2(f.z, f.w), make_float2(v[i + 2], v[i + 3]), a[1]);
-                }
-              }
-            }
-            ++it;
-          }
-          if (kq == kScaleBlocks - 1 || kb + 1 == c.kb1) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sempty_bar[sit & 1]);
-            ++sit;
-          }
-        }
-        if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < 128; i += 16)
-          if (i < hn) emit(acc + i, h0 + i);
-      } else if (OP == kTN && !cut) {
+      if (OP == kTN && !cut) {
         // 32 rows x 128 bytes at a time through a swizzled stage (two, in turn) and a TMA store,
         // which leaves out what lies past n and k
         constexpr int kStep = 128 / static_cast<int>(sizeof(OUT));
@@ -1150,22 +1033,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
       }
-      for (int n0 = h0; n0 < h0 + hn; n0 += 16) {
+      for (int n0 = 0; n0 < cols; n0 += 16) {
         float v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = 0.f;
-        for (int owner = first; owner <= last; owner += 2) {      // two parts' loads in flight
-          const float* a = slot(owner) + n0 * 128;
-          const float* b = slot(min(owner + 1, last)) + n0 * 128;
-          float x[16], y[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            x[i] = __ldcg(a + i * 128);
-            y[i] = owner < last ? __ldcg(b + i * 128) : 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = (v[i] + x[i]) + y[i];
-        }
+        join_parts(v, slot, first, last, n0);
         finish(v, n0);
       }
     }
@@ -1177,15 +1047,316 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<F8, OP>::kTh
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
+// ------------------------------------------------------------------ fold kernel
+// The e4m3 product on groups of more rows: 128 weight rows x up to 256 tokens per CTA.  Every K
+// block's products pass once through the epilogue, acc += (s_a s_w) x products, so what counts is
+// the round trip MMA - commit - TMEM load - release of a buffer.  The tile's tokens are two
+// halves of up to 128 with two TMEM buffers each; four epilogue warps fold either half, 128
+// fp32 sums per thread.  (The same on CTA pairs measured 446 us against the figures at the
+// launch: two hops between the CTAs per round trip cost more than the halved operand traffic
+// saves.)
+struct FoldCfg {
+  static constexpr int kWidth = 256;
+  static constexpr uint32_t kStage = kTileA + kWidth * 128;       // 48 KB
+  static constexpr int kStages = 4;
+  static constexpr int kCols = 128;                               // per buffer: one half
+  static constexpr int kThreads = 384;
+  // an epilogue thread keeps 128 sums and 32 products: registers move from warps 0..3 to 4..11.
+  // 384 x 168 at launch = 128 x 88 + 256 x 208.
+  static constexpr int kRegsLow = 88, kRegsHigh = 208;
+  static constexpr int kScaleRun = 4;                             // K blocks of scales at a time
+  static constexpr uint32_t kScales = 2 * kScaleRun * kWidth * 4;
+  static constexpr uint32_t kWarpStage = 1024;
+  static constexpr uint32_t kStaging = 8 * kWarpStage;
+  static constexpr uint32_t kSmem =
+      1024 + kStages * kStage + 1024 + kScales + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
+  static_assert(kSmem <= 227 * 1024, "budget");
+};
+
+// The halves of a tile of `rows` tokens: the first holds half_width of them; both are loaded in
+// whole 16-row steps.
+__device__ __forceinline__ int half_width(int rows) { return ((rows + 1) / 2 + 15) & ~15; }
+
+template <typename OUT>
+__global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid_constant__ ProductArgs p) {
+  using C = FoldCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(tiles + C::kStages * C::kStage);
+  uint64_t* empty_bar = full_bar + C::kStages;
+  uint64_t* tfull_bar = empty_bar + C::kStages;       // [half][2]
+  uint64_t* tempty_bar = tfull_bar + 4;
+  uint64_t* sfull_bar = tempty_bar + 4;
+  uint64_t* sempty_bar = sfull_bar + 2;
+  uint64_t* epi_bar = sempty_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* last_flag = reinterpret_cast<int*>(tmem_slot + 2);
+  float* scales = reinterpret_cast<float*>(tiles + C::kStages * C::kStage + 1024);
+  uint8_t* staging = reinterpret_cast<uint8_t*>(scales) + C::kScales;
+  GroupTable& gt = *reinterpret_cast<GroupTable*>(staging + C::kStaging);
+  int* status = p.header;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full_bar[i], 1);
+      mbar_init(&empty_bar[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&tfull_bar[i], 1);
+      mbar_init(&tempty_bar[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sfull_bar[i], 1);
+      mbar_init(&sempty_bar[i], 8);
+    }
+    mbar_init(epi_bar, 8);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.wmap);
+    tma_prefetch_desc(&p.tmap[0]);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  const int m_blocks = (p.m_total + 127) / 128;
+  const int n_tiles = build_groups(p, gt, C::kWidth, 32, 8, m_blocks, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  RoundShare sched(blockIdx.x, gridDim.x, n_tiles, p.k_blocks, true);
+  Piece c;
+  Tile t;
+  auto fetch = [&]() {
+    if (!sched.next(c)) return false;
+    t = token_tile(gt, c.tile, C::kWidth, 32, m_blocks, 12);
+    return true;
+  };
+
+  if (warp < 4) {
+    regs_down<C::kRegsLow>();                    // (one instruction for the whole warpgroup)
+    if (warp == 0) {
+      // -------------------------------------------------------- TMA producer
+      const bool elected = elect_one();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      while (ok && fetch()) {
+        const int hw = half_width(t.rows), n_pad = hw + ((max(t.rows - hw, 0) + 15) & ~15);
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          ok = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
+          if (!ok) break;
+          uint8_t* st = tiles + stage * C::kStage;
+          uint64_t* bar = &full_bar[stage];
+          if (elected) {
+            mbar_arrive_expect_tx(bar, kTileA + n_pad * 128);
+            tma_load_3d(st, &p.wmap, bar, kb * 128, t.mb * 128, t.g);
+            for (int bi = 0, off = 0; bi < 4; ++bi) {             // boxes of 128, 64, 32, 16 rows
+              const int box = 128 >> bi;
+              while (n_pad - off >= box) {
+                tma_load_2d(st + kTileA + off * 128, &p.tmap[bi], bar, kb * 128, t.row0 + off);
+                off += box;
+              }
+            }
+          }
+          __syncwarp();
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      const bool elected = elect_one();
+      int stage = 0;
+      uint32_t phase = 0, it0 = 0, it1 = 0;      // buffers used by the first, second halves
+      bool ok = true;
+      while (ok && fetch()) {
+        const int hw = half_width(t.rows), left = t.rows - hw;
+        const uint32_t id0 = idesc_e4m3_f32(128, hw), id1 = idesc_e4m3_f32(128, (left + 15) & ~15);
+        for (int kb = c.kb0; kb < c.kb1; ++kb) {
+          const uint32_t b0 = it0 & 1u, b1 = 2u + (it1 & 1u);
+          ok = mbar_wait_warp(&full_bar[stage], phase, abort_flag, status) &&
+               mbar_wait_warp(&tempty_bar[b0], ((it0 >> 1) & 1u) ^ 1u, abort_flag, status);
+          if (!ok) break;
+          ++it0;
+          tc_fence_after();
+          const uint32_t sa = smem_u32(tiles) + stage * C::kStage, sb = sa + kTileA;
+          if (elected) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_e4m3(tmem + b0 * C::kCols, umma_desc_sw128(sa + kk * 32), umma_desc_sw128(sb + kk * 32), id0,
+                        kk ? 1u : 0u);
+            umma_commit(&tfull_bar[b0]);
+            if (left <= 0) umma_commit(&empty_bar[stage]);
+          }
+          __syncwarp();
+          if (left > 0) {
+            ok = mbar_wait_warp(&tempty_bar[b1], ((it1 >> 1) & 1u) ^ 1u, abort_flag, status);
+            if (!ok) break;
+            ++it1;
+            tc_fence_after();
+            if (elected) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_e4m3(tmem + b1 * C::kCols, umma_desc_sw128(sa + kk * 32),
+                          umma_desc_sw128(sb + hw * 128 + kk * 32), id1, kk ? 1u : 0u);
+              umma_commit(&tfull_bar[b1]);
+              umma_commit(&empty_bar[stage]);
+            }
+            __syncwarp();
+          }
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    } else if (warp == 2) {
+      // -------------------------------------------------------- scales
+      // For kScaleRun K blocks at a time: each token's scales times the weight block's, as
+      // [K block][token].
+      uint32_t it = 0;
+      bool ok = true;
+      while (ok && fetch()) {
+        const float* sw = p.w_scale + (static_cast<size_t>(t.g) * p.w_scale_rows + t.mb) * p.k_blocks;
+        for (int kb = c.kb0; kb < c.kb1; kb += C::kScaleRun, ++it) {
+          const bool w = mbar_wait(&sempty_bar[it & 1], ((it >> 1) & 1u) ^ 1u, abort_flag, status);
+          if (!__all_sync(0xffffffffu, w)) {
+            ok = false;
+            break;
+          }
+          float* dst = scales + (it & 1) * (C::kScaleRun * C::kWidth);
+          float ws[C::kScaleRun];
+#pragma unroll
+          for (int q = 0; q < C::kScaleRun; ++q) ws[q] = __ldg(sw + min(kb + q, c.kb1 - 1));
+          for (int n0 = 0; n0 < t.rows; n0 += 128) {
+            float s[4][C::kScaleRun];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float* sa = p.a_scale +
+                                static_cast<size_t>(t.row0 + min(n0 + j * 32 + lane, t.rows - 1)) * p.k_blocks;
+#pragma unroll
+              for (int q = 0; q < C::kScaleRun; ++q) s[j][q] = __ldg(sa + min(kb + q, c.kb1 - 1));
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int q = 0; q < C::kScaleRun; ++q) dst[q * C::kWidth + n0 + j * 32 + lane] = s[j][q] * ws[q];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfull_bar[it & 1]);
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue
+    regs_up<C::kRegsHigh>();
+    const int sub = warp & 3;                    // TMEM lane quadrant
+    const int half = (warp - 4) >> 2;            // half of the tile's tokens
+    uint8_t* stg = staging + (warp - 4) * C::kWarpStage;
+    EpilogueSync sync{epi_bar, abort_flag, status};
+    uint32_t it = 0, sit = 0;
+    bool ok = true;
+    while (ok && fetch()) {
+      const int hw = half_width(t.rows);
+      const int h0 = half * hw, hn = min(hw, t.rows - h0);        // this warp's tokens
+      float acc[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int kb = c.kb0; kb < c.kb1; ++kb) {
+        const int kq = (kb - c.kb0) % C::kScaleRun;
+        if (kq == 0) {
+          const bool w = mbar_wait(&sfull_bar[sit & 1], (sit >> 1) & 1u, abort_flag, status);
+          ok = __all_sync(0xffffffffu, w) != 0;
+          if (!ok) break;
+        }
+        if (hn > 0) {
+          const float* sc = scales + ((sit & 1) * C::kScaleRun + kq) * C::kWidth + h0;
+          const uint32_t b = 2 * half + (it & 1u);
+          const bool w = mbar_wait(&tfull_bar[b], (it >> 1) & 1u, abort_flag, status);
+          ok = __all_sync(0xffffffffu, w) != 0;
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {          // 32 columns at a time
+            if (q * 32 < hn) {
+              float4 f[8];                       // in flight before the products are waited for
+#pragma unroll
+              for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const float4*>(sc + q * 32 + 4 * i);
+              float v[32];
+              tmem_ld32(tb + q * 32, v);
+              if ((q + 1) * 32 >= hn) {          // the buffer is free again
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty_bar[b]);
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 g = f[i / 4];
+                float2* a = reinterpret_cast<float2*>(&acc[q * 32 + i]);
+                a[0] = fma2(make_float2(g.x, g.y), make_float2(v[i], v[i + 1]), a[0]);
+                a[1] = fma2(make_float2(g.z, g.w), make_float2(v[i + 2], v[i + 3]), a[1]);
+              }
+            }
+          }
+          ++it;
+        }
+        if (kq == C::kScaleRun - 1 || kb + 1 == c.kb1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty_bar[sit & 1]);
+          ++sit;
+        }
+      }
+      if (!ok) break;
+      const int m0 = t.mb * 128 + sub * 32;      // the warp's first output column
+      auto finish = [&](const float* v, int n0) {
+        if (m0 < p.m_total)
+          store_transposed<OUT>(static_cast<OUT*>(p.out) + static_cast<size_t>(t.row0 + n0) * p.ld_out + m0,
+                                p.ld_out, h0 + hn - n0, p.m_total - m0, v, stg, lane);
+      };
+      if (!sched.cut(c)) {
+#pragma unroll
+        for (int i = 0; i < 128; i += 16)
+          if (i < hn) finish(acc + i, h0 + i);
+        continue;
+      }
+      int first, last;
+      sched.owners(c.tile, first, last);
+      auto slot = [&](int owner) { return p.partials + owner * kPairPartFloats + sub * 32 + lane; };
+      float* mine = slot(blockIdx.x);
+#pragma unroll
+      for (int i = 0; i < 128; ++i)
+        if (i < hn) __stcg(mine + (h0 + i) * 128, acc[i]);
+      if (!arrive_last(p.header, first, last - first + 1, sync, last_flag, warp == 4 && lane == 0, lane, ok)) continue;
+      for (int n0 = h0; n0 < h0 + hn; n0 += 16) {
+        float v[16];
+        join_parts(v, slot, first, last, n0);
+        finish(v, n0);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
 // ------------------------------------------------------------------ host
 constexpr size_t kProductHeader = 256;
-constexpr int kStreamCtas = 148, kPairs = 74;   // most CTAs / pairs a launch uses
-static_assert(kStreamCtas <= kMaxCounters && 2 * kPairs <= kMaxCounters, "join counters");
+constexpr int kMaxCtas = 148;                   // most CTAs that a launch uses
+static_assert(kMaxCtas <= kMaxCounters, "join counters");
 
 size_t product_workspace() {
-  const size_t stream = sizeof(float) * 2 * kStreamCtas * StreamCfg<true, kNT>::kTileFloats;
-  const size_t pair = sizeof(float) * kPairs * 2 * kPairPartFloats;
-  return kProductHeader + (stream > pair ? stream : pair);
+  const size_t stream = 2 * StreamCfg<true, kNT>::kTileFloats;   // floats per CTA
+  return kProductHeader + sizeof(float) * kMaxCtas * (stream > kPairPartFloats ? stream : kPairPartFloats);
 }
 
 int device_sms() {
@@ -1224,14 +1395,13 @@ template <bool F8, int OP, typename OUT>
 cudaError_t launch_product(const ProductArgs& a, bool stream_tiles, cudaStream_t s) {
   const int sms = device_sms();
   if (sms < 2) return cudaErrorInvalidDevice;
+  const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   if constexpr (OP != kTN) {
     if (stream_tiles)
-      return launch_product_kernel(stream_kernel<F8, OP, OUT>, a, sms < kStreamCtas ? sms : kStreamCtas, 224,
-                                   StreamCfg<F8, OP>::kSmem, s);
+      return launch_product_kernel(stream_kernel<F8, OP, OUT>, a, ctas, 224, StreamCfg<F8, OP>::kSmem, s);
   }
-  const int pairs = sms / 2 < kPairs ? sms / 2 : kPairs;
-  return launch_product_kernel(pair_kernel<F8, OP, OUT>, a, 2 * pairs, PairCfg<F8, OP>::kThreads,
-                               PairCfg<F8, OP>::kSmem, s);
+  if constexpr (F8) return launch_product_kernel(fold_kernel<OUT>, a, ctas, FoldCfg::kThreads, FoldCfg::kSmem, s);
+  else return launch_product_kernel(pair_kernel<OP, OUT>, a, ctas / 2 * 2, PairCfg<OP>::kThreads, PairCfg<OP>::kSmem, s);
 }
 template <bool F8, int OP>
 moe_status launch_product(const ProductArgs& a, bool f32, bool stream_tiles, cudaStream_t s) {
