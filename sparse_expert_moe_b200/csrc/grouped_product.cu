@@ -1048,34 +1048,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
 }
 
 // ------------------------------------------------------------------ fold kernel
-// The e4m3 product on groups of more rows: 128 weight rows x up to 256 tokens per CTA.  Every K
-// block's products pass once through the epilogue, acc += (s_a s_w) x products, so what counts is
-// the round trip MMA - commit - TMEM load - release of a buffer.  The tile's tokens are two
-// halves of up to 128 with two TMEM buffers each; four epilogue warps fold either half, 128
-// fp32 sums per thread.  (The same on CTA pairs measured 446 us against the figures at the
-// launch: two hops between the CTAs per round trip cost more than the halved operand traffic
-// saves.)
+// The e4m3 product on groups of more rows: up to 128 tokens x 256 weight rows per CTA.  Every K
+// block's products pass once through the epilogue, acc += (s_a s_w) x products.  Here the tokens
+// are the MMA's M side: a thread then holds one token's row, so that the factor of a K block is
+// one value per thread and 128-column half.  (With the weights on M the factor changes from
+// column to column; reading 128 factors per thread and K block from shared memory took 1024 of
+// 2100 cycles, 446 us at T = 8192, n = 4096, k = 7168.)  The tile's columns are two halves of
+// 128, one 128-row weight block each, with two TMEM buffers of 128 columns; four epilogue warps
+// fold either half, 128 fp32 sums per thread, while the other buffer is written.
 struct FoldCfg {
-  static constexpr int kWidth = 256;
-  static constexpr uint32_t kStage = kTileA + kWidth * 128;       // 48 KB
+  static constexpr int kWidth = 128;                              // tokens
+  static constexpr uint32_t kStage = 3 * kTileA;                  // 128 token + 256 weight rows: 48 KB
   static constexpr int kStages = 4;
-  static constexpr int kCols = 128;                               // per buffer: one half
+  static constexpr int kCols = 128;                               // per buffer
   static constexpr int kThreads = 384;
   // an epilogue thread keeps 128 sums and 32 products: registers move from warps 0..3 to 4..11.
-  // 384 x 168 at launch = 128 x 88 + 256 x 208.
-  static constexpr int kRegsLow = 88, kRegsHigh = 208;
-  static constexpr int kScaleRun = 4;                             // K blocks of scales at a time
-  static constexpr uint32_t kScales = 2 * kScaleRun * kWidth * 4;
-  static constexpr uint32_t kWarpStage = 1024;
+  // 384 x 168 at launch = 128 x 56 + 256 x 224.
+  static constexpr int kRegsLow = 56, kRegsHigh = 224;
+  static constexpr uint32_t kWarpStage = 2048;
   static constexpr uint32_t kStaging = 8 * kWarpStage;
   static constexpr uint32_t kSmem =
-      1024 + kStages * kStage + 1024 + kScales + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
+      1024 + kStages * kStage + 1024 + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
   static_assert(kSmem <= 227 * 1024, "budget");
 };
-
-// The halves of a tile of `rows` tokens: the first holds half_width of them; both are loaded in
-// whole 16-row steps.
-__device__ __forceinline__ int half_width(int rows) { return ((rows + 1) / 2 + 15) & ~15; }
 
 template <typename OUT>
 __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid_constant__ ProductArgs p) {
@@ -1087,14 +1082,11 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
   uint64_t* empty_bar = full_bar + C::kStages;
   uint64_t* tfull_bar = empty_bar + C::kStages;       // [half][2]
   uint64_t* tempty_bar = tfull_bar + 4;
-  uint64_t* sfull_bar = tempty_bar + 4;
-  uint64_t* sempty_bar = sfull_bar + 2;
-  uint64_t* epi_bar = sempty_bar + 2;
+  uint64_t* epi_bar = tempty_bar + 4;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* last_flag = reinterpret_cast<int*>(tmem_slot + 2);
-  float* scales = reinterpret_cast<float*>(tiles + C::kStages * C::kStage + 1024);
-  uint8_t* staging = reinterpret_cast<uint8_t*>(scales) + C::kScales;
+  uint8_t* staging = tiles + C::kStages * C::kStage + 1024;
   GroupTable& gt = *reinterpret_cast<GroupTable*>(staging + C::kStaging);
   int* status = p.header;
 
@@ -1108,10 +1100,6 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
       mbar_init(&tfull_bar[i], 1);
       mbar_init(&tempty_bar[i], 4);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sfull_bar[i], 1);
-      mbar_init(&sempty_bar[i], 8);
-    }
     mbar_init(epi_bar, 8);
     *abort_flag = 0;
     fence_mbar_init();
@@ -1122,20 +1110,21 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  const int m_blocks = (p.m_total + 127) / 128;
-  const int n_tiles = build_groups(p, gt, C::kWidth, 32, 8, m_blocks, 0);
+  const int col_blocks = (p.m_total + 255) / 256;
+  const int n_tiles = build_groups(p, gt, C::kWidth, 16, 8, col_blocks, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   RoundShare sched(blockIdx.x, gridDim.x, n_tiles, p.k_blocks, true);
   Piece c;
-  Tile t;
+  Tile t;                                        // mb: block of 256 weight rows
   auto fetch = [&]() {
     if (!sched.next(c)) return false;
-    t = token_tile(gt, c.tile, C::kWidth, 32, m_blocks, 12);
+    t = token_tile(gt, c.tile, C::kWidth, 16, col_blocks, 8);
     return true;
   };
+  auto halves = [&]() { return p.m_total - t.mb * 256 > 128 ? 2 : 1; };
 
   if (warp < 4) {
     regs_down<C::kRegsLow>();                    // (one instruction for the whole warpgroup)
@@ -1146,19 +1135,20 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
       uint32_t phase = 0;
       bool ok = true;
       while (ok && fetch()) {
-        const int hw = half_width(t.rows), n_pad = hw + ((max(t.rows - hw, 0) + 15) & ~15);
+        const int n_pad = (t.rows + 15) & ~15, nh = halves();
         for (int kb = c.kb0; kb < c.kb1; ++kb) {
           ok = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
           if (!ok) break;
           uint8_t* st = tiles + stage * C::kStage;
           uint64_t* bar = &full_bar[stage];
           if (elected) {
-            mbar_arrive_expect_tx(bar, kTileA + n_pad * 128);
-            tma_load_3d(st, &p.wmap, bar, kb * 128, t.mb * 128, t.g);
+            mbar_arrive_expect_tx(bar, nh * kTileA + n_pad * 128);
+            tma_load_3d(st + kTileA, &p.wmap, bar, kb * 128, t.mb * 256, t.g);
+            if (nh > 1) tma_load_3d(st + 2 * kTileA, &p.wmap, bar, kb * 128, t.mb * 256 + 128, t.g);
             for (int bi = 0, off = 0; bi < 4; ++bi) {             // boxes of 128, 64, 32, 16 rows
               const int box = 128 >> bi;
               while (n_pad - off >= box) {
-                tma_load_2d(st + kTileA + off * 128, &p.tmap[bi], bar, kb * 128, t.row0 + off);
+                tma_load_2d(st + off * 128, &p.tmap[bi], bar, kb * 128, t.row0 + off);
                 off += box;
               }
             }
@@ -1172,13 +1162,15 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
       }
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
+      // Rows of the token tile that were not loaded hold what an earlier stage left: their
+      // products stay in TMEM lanes that nobody stores.
       const bool elected = elect_one();
+      const uint32_t idesc = idesc_e4m3_f32(128, 128);
       int stage = 0;
       uint32_t phase = 0, it0 = 0, it1 = 0;      // buffers used by the first, second halves
       bool ok = true;
       while (ok && fetch()) {
-        const int hw = half_width(t.rows), left = t.rows - hw;
-        const uint32_t id0 = idesc_e4m3_f32(128, hw), id1 = idesc_e4m3_f32(128, (left + 15) & ~15);
+        const int nh = halves();
         for (int kb = c.kb0; kb < c.kb1; ++kb) {
           const uint32_t b0 = it0 & 1u, b1 = 2u + (it1 & 1u);
           ok = mbar_wait_warp(&full_bar[stage], phase, abort_flag, status) &&
@@ -1190,13 +1182,13 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
           if (elected) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              umma_e4m3(tmem + b0 * C::kCols, umma_desc_sw128(sa + kk * 32), umma_desc_sw128(sb + kk * 32), id0,
+              umma_e4m3(tmem + b0 * C::kCols, umma_desc_sw128(sa + kk * 32), umma_desc_sw128(sb + kk * 32), idesc,
                         kk ? 1u : 0u);
             umma_commit(&tfull_bar[b0]);
-            if (left <= 0) umma_commit(&empty_bar[stage]);
+            if (nh == 1) umma_commit(&empty_bar[stage]);
           }
           __syncwarp();
-          if (left > 0) {
+          if (nh > 1) {
             ok = mbar_wait_warp(&tempty_bar[b1], ((it1 >> 1) & 1u) ^ 1u, abort_flag, status);
             if (!ok) break;
             ++it1;
@@ -1205,7 +1197,7 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 umma_e4m3(tmem + b1 * C::kCols, umma_desc_sw128(sa + kk * 32),
-                          umma_desc_sw128(sb + hw * 128 + kk * 32), id1, kk ? 1u : 0u);
+                          umma_desc_sw128(sb + kTileA + kk * 32), idesc, kk ? 1u : 0u);
               umma_commit(&tfull_bar[b1]);
               umma_commit(&empty_bar[stage]);
             }
@@ -1217,129 +1209,91 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
           }
         }
       }
-    } else if (warp == 2) {
-      // -------------------------------------------------------- scales
-      // For kScaleRun K blocks at a time: each token's scales times the weight block's, as
-      // [K block][token].
-      uint32_t it = 0;
-      bool ok = true;
-      while (ok && fetch()) {
-        const float* sw = p.w_scale + (static_cast<size_t>(t.g) * p.w_scale_rows + t.mb) * p.k_blocks;
-        for (int kb = c.kb0; kb < c.kb1; kb += C::kScaleRun, ++it) {
-          const bool w = mbar_wait(&sempty_bar[it & 1], ((it >> 1) & 1u) ^ 1u, abort_flag, status);
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
-          }
-          float* dst = scales + (it & 1) * (C::kScaleRun * C::kWidth);
-          float ws[C::kScaleRun];
-#pragma unroll
-          for (int q = 0; q < C::kScaleRun; ++q) ws[q] = __ldg(sw + min(kb + q, c.kb1 - 1));
-          for (int n0 = 0; n0 < t.rows; n0 += 128) {
-            float s[4][C::kScaleRun];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float* sa = p.a_scale +
-                                static_cast<size_t>(t.row0 + min(n0 + j * 32 + lane, t.rows - 1)) * p.k_blocks;
-#pragma unroll
-              for (int q = 0; q < C::kScaleRun; ++q) s[j][q] = __ldg(sa + min(kb + q, c.kb1 - 1));
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int q = 0; q < C::kScaleRun; ++q) dst[q * C::kWidth + n0 + j * 32 + lane] = s[j][q] * ws[q];
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sfull_bar[it & 1]);
-        }
-      }
-      __syncwarp();
     }
   } else {
     // ---------------------------------------------------------- epilogue
     regs_up<C::kRegsHigh>();
-    const int sub = warp & 3;                    // TMEM lane quadrant
-    const int half = (warp - 4) >> 2;            // half of the tile's tokens
+    constexpr int kRun = 4;                      // K blocks of scales fetched at a time
+    const int sub = warp & 3;                    // TMEM lane quadrant: tokens sub * 32 + lane
+    const int half = (warp - 4) >> 2;            // 128-column half of the tile
     uint8_t* stg = staging + (warp - 4) * C::kWarpStage;
     EpilogueSync sync{epi_bar, abort_flag, status};
-    uint32_t it = 0, sit = 0;
+    uint32_t it = 0;
     bool ok = true;
     while (ok && fetch()) {
-      const int hw = half_width(t.rows);
-      const int h0 = half * hw, hn = min(hw, t.rows - h0);        // this warp's tokens
+      const int col0 = t.mb * 256 + half * 128;  // the warp's first output column
+      const int rows = t.rows - sub * 32;        // its rows (<= 0: none)
+      const bool here = half < halves();
+      const bool mine = here && rows > 0;
       float acc[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-      for (int kb = c.kb0; kb < c.kb1; ++kb) {
-        const int kq = (kb - c.kb0) % C::kScaleRun;
-        if (kq == 0) {
-          const bool w = mbar_wait(&sfull_bar[sit & 1], (sit >> 1) & 1u, abort_flag, status);
-          ok = __all_sync(0xffffffffu, w) != 0;
-          if (!ok) break;
+      const float* sa = p.a_scale + static_cast<size_t>(t.row0 + min(sub * 32 + lane, t.rows - 1)) * p.k_blocks;
+      const float* sw = p.w_scale + (static_cast<size_t>(t.g) * p.w_scale_rows +
+                                     min(2 * t.mb + half, p.w_scale_rows - 1)) * p.k_blocks;
+      float next_a[kRun], next_w[kRun], f[kRun];
+      auto scales = [&](int kb) {
+#pragma unroll
+        for (int q = 0; q < kRun; ++q) {
+          next_a[q] = __ldg(sa + min(kb + q, c.kb1 - 1));
+          next_w[q] = __ldg(sw + min(kb + q, c.kb1 - 1));
         }
-        if (hn > 0) {
-          const float* sc = scales + ((sit & 1) * C::kScaleRun + kq) * C::kWidth + h0;
-          const uint32_t b = 2 * half + (it & 1u);
-          const bool w = mbar_wait(&tfull_bar[b], (it >> 1) & 1u, abort_flag, status);
-          ok = __all_sync(0xffffffffu, w) != 0;
-          if (!ok) break;
-          tc_fence_after();
+      };
+      if (mine) scales(c.kb0);
+      for (int kb = c.kb0; kb < c.kb1 && here; ++kb, ++it) {
+        const int kq = (kb - c.kb0) % kRun;
+        if (mine && kq == 0) {
+#pragma unroll
+          for (int q = 0; q < kRun; ++q) f[q] = next_a[q] * next_w[q];
+          if (kb + kRun < c.kb1) scales(kb + kRun);
+        }
+        const uint32_t b = 2 * half + (it & 1u);
+        ok = mbar_wait_warp(&tfull_bar[b], (it >> 1) & 1u, abort_flag, status);
+        if (!ok) break;
+        tc_fence_after();
+        if (mine) {
           const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
+          const float g = kq == 0 ? f[0] : (kq == 1 ? f[1] : (kq == 2 ? f[2] : f[3]));
+          const float2 gg = make_float2(g, g);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {          // 32 columns at a time
-            if (q * 32 < hn) {
-              float4 f[8];                       // in flight before the products are waited for
+          for (int q = 0; q < 4; ++q) {
+            float v[32];
+            tmem_ld32(tb + q * 32, v);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] = *reinterpret_cast<const float4*>(sc + q * 32 + 4 * i);
-              float v[32];
-              tmem_ld32(tb + q * 32, v);
-              if ((q + 1) * 32 >= hn) {          // the buffer is free again
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty_bar[b]);
-              }
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 g = f[i / 4];
-                float2* a = reinterpret_cast<float2*>(&acc[q * 32 + i]);
-                a[0] = fma2(make_float2(g.x, g.y), make_float2(v[i], v[i + 1]), a[0]);
-                a[1] = fma2(make_float2(g.z, g.w), make_float2(v[i + 2], v[i + 3]), a[1]);
-              }
+            for (int i = 0; i < 32; i += 2) {
+              float2* a = reinterpret_cast<float2*>(&acc[q * 32 + i]);
+              *a = fma2(gg, make_float2(v[i], v[i + 1]), *a);
             }
           }
-          ++it;
+          tc_fence_before();
         }
-        if (kq == C::kScaleRun - 1 || kb + 1 == c.kb1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sempty_bar[sit & 1]);
-          ++sit;
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty_bar[b]);   // the buffer is free again
       }
       if (!ok) break;
-      const int m0 = t.mb * 128 + sub * 32;      // the warp's first output column
-      auto finish = [&](const float* v, int n0) {
-        if (m0 < p.m_total)
-          store_transposed<OUT>(static_cast<OUT*>(p.out) + static_cast<size_t>(t.row0 + n0) * p.ld_out + m0,
-                                p.ld_out, h0 + hn - n0, p.m_total - m0, v, stg, lane);
+      auto finish = [&](const float* v, int i) {
+        if (mine && col0 + i < p.m_total)
+          store_direct<OUT>(static_cast<OUT*>(p.out) + static_cast<size_t>(t.row0 + sub * 32) * p.ld_out + col0 + i,
+                            p.ld_out, rows, p.m_total - col0 - i, v, stg, lane);
       };
       if (!sched.cut(c)) {
 #pragma unroll
-        for (int i = 0; i < 128; i += 16)
-          if (i < hn) finish(acc + i, h0 + i);
+        for (int i = 0; i < 128; i += 16) finish(acc + i, i);
         continue;
       }
       int first, last;
       sched.owners(c.tile, first, last);
       auto slot = [&](int owner) { return p.partials + owner * kPairPartFloats + sub * 32 + lane; };
-      float* mine = slot(blockIdx.x);
+      if (mine) {
+        float* to = slot(blockIdx.x) + half * 128 * 128;
 #pragma unroll
-      for (int i = 0; i < 128; ++i)
-        if (i < hn) __stcg(mine + (h0 + i) * 128, acc[i]);
+        for (int i = 0; i < 128; ++i) __stcg(to + i * 128, acc[i]);
+      }
       if (!arrive_last(p.header, first, last - first + 1, sync, last_flag, warp == 4 && lane == 0, lane, ok)) continue;
-      for (int n0 = h0; n0 < h0 + hn; n0 += 16) {
+      for (int i = 0; i < 128 && mine; i += 16) {
         float v[16];
-        join_parts(v, slot, first, last, n0);
-        finish(v, n0);
+        join_parts(v, slot, first, last, half * 128 + i);
+        finish(v, i);
       }
     }
   }
