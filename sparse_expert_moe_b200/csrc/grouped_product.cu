@@ -359,6 +359,39 @@ __device__ __forceinline__ bool arrive_last(int* header, int counter, int n, Epi
   return last;
 }
 
+// A cut tile's fp32 sums in the workspace: four consecutive columns of a row together, rows next
+// to one another, [columns / 4][128 rows][4].  `slot` is this thread's row of one part.
+__device__ __forceinline__ void write_part(float* slot, int col, const float* v) {   // 4 columns
+  __stcg(reinterpret_cast<float4*>(slot + col * 128), make_float4(v[0], v[1], v[2], v[3]));
+}
+// N columns from `col` of which `valid` count: the sums of parts first .. last, added in order,
+// with kDeep parts' loads in flight.
+template <int N, int kDeep, class Slot>
+__device__ __forceinline__ void join_parts(float* v, Slot slot, int first, int last, int col, int valid) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.f;
+  for (int part = first; part <= last; part += kDeep) {
+    float4 x[kDeep][N / 4];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const float* from = slot(min(part + d, last)) + col * 128;
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i)
+        x[d][i] = part + d <= last && 4 * i < valid ? __ldcg(reinterpret_cast<const float4*>(from + i * 512))
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        v[4 * i] += x[d][i].x;
+        v[4 * i + 1] += x[d][i].y;
+        v[4 * i + 2] += x[d][i].z;
+        v[4 * i + 3] += x[d][i].w;
+      }
+  }
+}
+
 // ------------------------------------------------------------------ stream kernel
 template <bool F8, int OP>
 struct StreamCfg {
@@ -621,31 +654,21 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
         int first, last;
         sched.owners(c.tile, first, last);
         auto slot = [&](int cta) {
-          return p.partials + (static_cast<size_t>(cta) * 2 + (cta == first ? 1 : 0)) * C::kTileFloats + m_local;
+          return p.partials + (static_cast<size_t>(cta) * 2 + (cta == first ? 1 : 0)) * C::kTileFloats + m_local * 4;
         };
         float* mine = slot(blockIdx.x);
 #pragma unroll
         for (int j = 0; j < C::kMB; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (h * 16 < t.rows)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) __stcg(mine + (j * C::kNTok + h * 16 + i) * 128, acc[j][h][i]);
+          for (int i = 0; i < 32; i += 4)
+            if (i < t.rows) write_part(mine, j * C::kNTok + i, &acc[j][i >> 4][i & 15]);
         if (!arrive_last(p.header, first, last - first + 1, sync, last_flag, m_local == 0, lane, ok)) continue;
 #pragma unroll
         for (int j = 0; j < C::kMB; ++j)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[j][0][i] = acc[j][1][i] = 0.f;
-        for (int cta = first; cta <= last; ++cta) {
-          const float* part = slot(cta);
-#pragma unroll
-          for (int j = 0; j < C::kMB; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (h * 16 < t.rows)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[j][h][i] += __ldcg(part + (j * C::kNTok + h * 16 + i) * 128);
-        }
+          for (int h = 0; h < 2; ++h)
+            if (h * 16 < t.rows)
+              join_parts<16, 4>(acc[j][h], slot, first, last, j * C::kNTok + h * 16, t.rows - h * 16);
       }
 #pragma unroll
       for (int j = 0; j < C::kMB; ++j) {
@@ -664,28 +687,9 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
   if (warp == 1) tmem_dealloc(tmem, C::kTmem);
 }
 
-constexpr size_t kPairPartFloats = 128 * 256;   // a CTA's fp32 sums of a cut tile, [column][row]
-
-// Sixteen columns of a cut tile: the sums of its parts, added in order, two parts' loads in flight.
-template <class Slot>
-__device__ __forceinline__ void join_parts(float (&v)[16], Slot slot, int first, int last, int n0) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = 0.f;
-  for (int owner = first; owner <= last; owner += 2) {
-    const float* a = slot(owner) + n0 * 128;
-    const float* b = slot(min(owner + 1, last)) + n0 * 128;
-    float x[16], y[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      x[i] = __ldcg(a + i * 128);
-      y[i] = owner < last ? __ldcg(b + i * 128) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = (v[i] + x[i]) + y[i];
-  }
-}
-
 // ------------------------------------------------------------------ pair kernel
+constexpr size_t kPartFloats = 128 * 256;       // a CTA's sums of a cut tile
+
 template <int OP>
 struct PairCfg {
   static constexpr int kWidth = 256;                              // tokens (TN: columns) per tile
@@ -939,7 +943,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
       int first = 0, last = 0;
       if (cut) sched.owners(c.tile, first, last);
       auto slot = [&](int owner) {
-        return p.partials + (static_cast<size_t>(owner) * 2 + rank) * kPairPartFloats + m_local;
+        return p.partials + (static_cast<size_t>(owner) * 2 + rank) * kPartFloats + m_local * 4;
       };
       // sixteen columns of the finished tile to global memory
       auto finish = [&](const float* v, int n0) {
@@ -958,7 +962,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
         } else {
           float* mine = slot(pair);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) __stcg(mine + (n0 + i) * 128, v[i]);
+          for (int i = 0; i < 16; i += 4) write_part(mine, n0 + i, v + i);
         }
       };
       if (OP == kTN && !cut) {
@@ -1033,10 +1037,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
       }
-      for (int n0 = 0; n0 < cols; n0 += 16) {
-        float v[16];
-        join_parts(v, slot, first, last, n0);
+      for (int n0 = 0; n0 < cols; n0 += 32) {
+        float v[32];
+        join_parts<32, 2>(v, slot, first, last, n0, cols - n0);
         finish(v, n0);
+        if (n0 + 16 < cols) finish(v + 16, n0 + 16);
       }
     }
     if (OP == kTN && lane == 0) bulk_wait_all();
@@ -1283,17 +1288,18 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
       }
       int first, last;
       sched.owners(c.tile, first, last);
-      auto slot = [&](int owner) { return p.partials + owner * kPairPartFloats + sub * 32 + lane; };
+      auto slot = [&](int owner) { return p.partials + owner * kPartFloats + (sub * 32 + lane) * 4; };
       if (mine) {
-        float* to = slot(blockIdx.x) + half * 128 * 128;
+        float* to = slot(blockIdx.x);
 #pragma unroll
-        for (int i = 0; i < 128; ++i) __stcg(to + i * 128, acc[i]);
+        for (int i = 0; i < 128; i += 4) write_part(to, half * 128 + i, acc + i);
       }
       if (!arrive_last(p.header, first, last - first + 1, sync, last_flag, warp == 4 && lane == 0, lane, ok)) continue;
-      for (int i = 0; i < 128 && mine; i += 16) {
-        float v[16];
-        join_parts(v, slot, first, last, half * 128 + i);
+      for (int i = 0; i < 128 && mine; i += 32) {
+        float v[32];
+        join_parts<32, 2>(v, slot, first, last, half * 128 + i, 32);
         finish(v, i);
+        finish(v + 16, i + 16);
       }
     }
   }
@@ -1310,7 +1316,7 @@ static_assert(kMaxCtas <= kMaxCounters, "join counters");
 
 size_t product_workspace() {
   const size_t stream = 2 * StreamCfg<true, kNT>::kTileFloats;   // floats per CTA
-  return kProductHeader + sizeof(float) * kMaxCtas * (stream > kPairPartFloats ? stream : kPairPartFloats);
+  return kProductHeader + sizeof(float) * kMaxCtas * (stream > kPartFloats ? stream : kPartFloats);
 }
 
 int device_sms() {
