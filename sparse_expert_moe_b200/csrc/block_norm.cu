@@ -83,6 +83,11 @@ __device__ __forceinline__ float load1(const void* base, size_t i, bool f32) {
              : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
 }
 
+// A value that the CTA's threads will load in some turns' time.
+__device__ __forceinline__ void prefetch_l1(const void* base, size_t i, bool f32) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const char*>(base) + i * (f32 ? 4 : 2)));
+}
+
 // Sums of N values over the threads of a row, the same in every thread of it and in the same
 // order every time.  `part`: shared memory, N floats per warp of the CTA, not touched since
 // the __syncthreads before the call before last.  All threads of the CTA call this.
@@ -172,6 +177,7 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
         if (p.y) stage_in<ACT32>(st + kAtY * threads, j, threads, p.y, base + v);
         if (full_gate) stage_in<ACT32>(st + kAtGate * threads, j, threads, p.gate, base + v);
       }
+      if (p.gate_kind == MOE_GATE_TOKEN && i0 == 0) prefetch_l1(p.gate, t, p.w_f32);
     }
     rows_commit();
   };
@@ -219,10 +225,12 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
     return s2.x + s2.y;
   };
   // B: r' of row t into r and out, and this thread's part of the sum of its squares
-  auto residual = [&](int t, const uint4* st, float tok) {       // tok = i_y (token gate)
+  auto residual = [&](int t, const uint4* st, float i_y) {
     float2 s2 = both(0.f);
     if (t >= p.T) return 0.f;
     const size_t base = static_cast<size_t>(t) * p.nvec;
+    float tok = i_y;
+    if (p.gate_kind == MOE_GATE_TOKEN) tok *= load1(p.gate, t, p.w_f32);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
@@ -282,9 +290,6 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
     }
   };
   auto i_of = [&](float ss) { return p.w_post ? rsqrtf(fmaf(ss, p.inv_d, p.eps)) : 1.f; };
-  auto token_gate = [&](int t) {
-    return p.gate_kind == MOE_GATE_TOKEN && t < p.T ? load1(p.gate, t, p.w_f32) : 1.f;
-  };
 
   if (!kStaged) {                              // one row per row slot
     const int t = blockIdx.x * p.rows + row;
@@ -293,13 +298,12 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
       for (int j = 0; j < VPT; ++j)
         if (i0 + j * p.tpr < p.nvec) r[j] = load8(p.r, static_cast<size_t>(t) * p.nvec + i0 + j * p.tpr, RES32);
     }
-    const float g = token_gate(t);
     float sy[1] = {0.f};
     if (p.w_post) {
       sy[0] = branch_square(t, nullptr);
       row_sums(sy, part[0], p.tpr);
     }
-    float sr[1] = {residual(t, nullptr, i_of(sy[0]) * g)};
+    float sr[1] = {residual(t, nullptr, i_of(sy[0]))};
     if (!p.w_pre) return;
     row_sums(sr, part[1], p.tpr);
     normalised(t, sr[0]);
@@ -313,15 +317,12 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
   float sums[2] = {0.f, p.w_post ? branch_square(t, ring + threadIdx.x) : 0.f};
   if (p.w_post) row_sums(sums, part[1], p.tpr);
   int turn = 0;
-  float g = token_gate(t);
   for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, t += step, ++turn) {
-    const float g_next = token_gate(t + step);
     fetch(t + (kStages - 1) * step, (turn + kStages - 1) % kRing);
     rows_wait<kStages>();                      // row t + step
     const uint4* st = ring + turn % kRing * stage_vecs + threadIdx.x;
     const uint4* next = ring + (turn + 1) % kRing * stage_vecs + threadIdx.x;
-    sums[0] = residual(t, st, i_of(sums[1]) * g);
-    g = g_next;
+    sums[0] = residual(t, st, i_of(sums[1]));
     if (p.w_post) {
       sums[1] = branch_square(t + step, next);
       row_sums(sums, part[turn & 1], p.tpr);
@@ -401,6 +402,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
         if (p.y) stage_in<ACT32>(st + kAtY * threads, j, threads, p.y, base + v);
         if (full_gate) stage_in<ACT32>(st + kAtGate * threads, j, threads, p.gate, base + v);
       }
+      if (p.gate_kind == MOE_GATE_TOKEN && i0 == 0) prefetch_l1(p.gate, t, p.w_f32);
     }
     rows_commit();
   };
@@ -470,11 +472,13 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
     s[2] = s2.x + s2.y;
   };
   // 2: G of row t (dr, the channel sums), q kept, and the parts of the sums of q y and G u
-  auto gradients = [&](int t, const uint4* st, float tok, float i_r, float zr, float i_y, float* m) {
+  auto gradients = [&](int t, const uint4* st, float i_r, float zr, float i_y, float* m) {
     m[0] = m[1] = 0.f;
     if (t >= p.T) return;
     const size_t base = static_cast<size_t>(t) * p.nvec;
     const float2 k_r = both(-i_r * i_r * i_r * (zr * p.inv_d));
+    float tok = p.branch_scale;
+    if (p.gate_kind == MOE_GATE_TOKEN) tok *= load1(p.gate, t, p.w_f32);
     float2 m0 = both(0.f), m1 = both(0.f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -554,10 +558,6 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
     }
   };
   auto i_of = [&](float ss) { return rsqrtf(fmaf(ss, p.inv_d, p.eps)); };
-  auto scale_of = [&](int t) {                 // branch_scale (token gate)
-    return p.gate_kind == MOE_GATE_TOKEN && t < p.T ? p.branch_scale * load1(p.gate, t, p.w_f32) : p.branch_scale;
-  };
-
   int t = blockIdx.x * p.rows + row;
   if (!kStaged) {
     // every thread of the CTA makes the same number of turns (row_sums synchronises it)
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
       squares(t, nullptr, s);
       row_sums(s, part[0], p.tpr);
       const float i_y = p.w_post ? i_of(s[2]) : 1.f;
-      gradients(t, nullptr, scale_of(t), i_of(s[0]), s[1], i_y, m);
+      gradients(t, nullptr, i_of(s[0]), s[1], i_y, m);
       row_sums(m, part[1], p.tpr);
       branch_gradient(t, nullptr, i_y, m[0], m[1]);
     }
@@ -583,15 +583,12 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
       s[2] = f[2];
     }
     int turn = 0;
-    float tok = scale_of(t);
     for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, t += step, ++turn) {
-      const float tok_next = scale_of(t + step);
       fetch(t + (kStages - 1) * step, (turn + kStages - 1) % kRing);
       rows_wait<kStages>();                    // row t + step
       const uint4* st = ring + turn % kRing * stage_vecs + threadIdx.x;
       const float i_y = p.w_post ? i_of(s[2]) : 1.f;
-      gradients(t, st, tok, i_of(s[0]), s[1], i_y, s + 3);
-      tok = tok_next;
+      gradients(t, st, i_of(s[0]), s[1], i_y, s + 3);
       squares(t + step, ring + (turn + 1) % kRing * stage_vecs + threadIdx.x, s);
       row_sums(s, part[turn & 1], p.tpr);
       branch_gradient(t, st, i_y, s[3], s[4]);
