@@ -39,25 +39,20 @@ struct NormArgs {
 
 // Eight consecutive elements as four pairs.
 struct Vec8 {
-  float2 p[4];
+  f32x2 p[4];
 };
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ Vec8 constant8(float v) {
-  return Vec8{{both(v), both(v), both(v), both(v)}};
+  return Vec8{{both2(v), both2(v), both2(v), both2(v)}};
 }
 __device__ __forceinline__ Vec8 unpack_bf16(const uint4& a) {
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
   Vec8 f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    f.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  for (int i = 0; i < 4; ++i) f.p[i] = pack2(w[i] << 16, w[i] & 0xFFFF0000u);
   return f;
 }
 __device__ __forceinline__ Vec8 unpack_f32(const uint4& a, const uint4& b) {
-  return Vec8{{make_float2(__uint_as_float(a.x), __uint_as_float(a.y)),
-               make_float2(__uint_as_float(a.z), __uint_as_float(a.w)),
-               make_float2(__uint_as_float(b.x), __uint_as_float(b.y)),
-               make_float2(__uint_as_float(b.z), __uint_as_float(b.w))}};
+  return Vec8{{pack2(a.x, a.y), pack2(a.z, a.w), pack2(b.x, b.y), pack2(b.z, b.w)}};
 }
 // Vector `v` (elements 8 v .. 8 v + 7) of a bf16 or fp32 array.
 __device__ __forceinline__ Vec8 load8(const void* base, size_t v, bool f32) {
@@ -65,15 +60,18 @@ __device__ __forceinline__ Vec8 load8(const void* base, size_t v, bool f32) {
   return f32 ? unpack_f32(q[2 * v], q[2 * v + 1]) : unpack_bf16(q[v]);
 }
 __device__ __forceinline__ void store8(void* base, size_t v, bool f32, const Vec8& f) {
+  const float2 a = unpack2(f.p[0]), b = unpack2(f.p[1]), c = unpack2(f.p[2]), d = unpack2(f.p[3]);
   if (f32) {
     float4* o = static_cast<float4*>(base) + 2 * v;
-    o[0] = make_float4(f.p[0].x, f.p[0].y, f.p[1].x, f.p[1].y);
-    o[1] = make_float4(f.p[2].x, f.p[2].y, f.p[3].x, f.p[3].y);
+    o[0] = make_float4(a.x, a.y, b.x, b.y);
+    o[1] = make_float4(c.x, c.y, d.x, d.y);
   } else {
     uint4 q;
-    __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(f.p[i].x, f.p[i].y);
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
+    h[0] = __floats2bfloat162_rn(a.x, a.y);
+    h[1] = __floats2bfloat162_rn(b.x, b.y);
+    h[2] = __floats2bfloat162_rn(c.x, c.y);
+    h[3] = __floats2bfloat162_rn(d.x, d.y);
     static_cast<uint4*>(base)[v] = q;
   }
 }
@@ -81,11 +79,6 @@ __device__ __forceinline__ void store8(void* base, size_t v, bool f32, const Vec
 __device__ __forceinline__ float load1(const void* base, size_t i, bool f32) {
   return f32 ? static_cast<const float*>(base)[i]
              : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
-}
-
-// A value that the CTA's threads will load in some turns' time.
-__device__ __forceinline__ void prefetch_l1(const void* base, size_t i, bool f32) {
-  asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const char*>(base) + i * (f32 ? 4 : 2)));
 }
 
 // Sums of N values over the threads of a row, the same in every thread of it and in the same
@@ -177,7 +170,6 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
         if (p.y) stage_in<ACT32>(st + kAtY * threads, j, threads, p.y, base + v);
         if (full_gate) stage_in<ACT32>(st + kAtGate * threads, j, threads, p.gate, base + v);
       }
-      if (p.gate_kind == MOE_GATE_TOKEN && i0 == 0) prefetch_l1(p.gate, t, p.w_f32);
     }
     rows_commit();
   };
@@ -195,7 +187,7 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
       const Vec8 a = load8(p.w_post, v, p.w_f32);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        c[j].p[e] = mul2(c[j].p[e], make_float2(a.p[e].x + p.w_offset, a.p[e].y + p.w_offset));
+        c[j].p[e] = mul2(c[j].p[e], add2(a.p[e], both2(p.w_offset)));
     }
     if (p.gate_kind == MOE_GATE_CHANNEL) {
       const Vec8 a = load8(p.gate, v, p.w_f32);
@@ -205,14 +197,14 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
     if (p.w_pre) {
       w[j] = load8(p.w_pre, v, p.w_f32);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[j].p[e] = make_float2(w[j].p[e].x + p.w_offset, w[j].p[e].y + p.w_offset);
+      for (int e = 0; e < 4; ++e) w[j].p[e] = add2(w[j].p[e], both2(p.w_offset));
     }
   }
 
   Vec8 r[VPT];
   // A: this thread's part of the sum of y^2 of row t
   auto branch_square = [&](int t, const uint4* st) {
-    float2 s2 = both(0.f);
+    f32x2 s2 = both2(0.f);
     const size_t base = static_cast<size_t>(t) * p.nvec;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -222,15 +214,13 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
 #pragma unroll
       for (int e = 0; e < 4; ++e) s2 = fma2(y.p[e], y.p[e], s2);
     }
-    return s2.x + s2.y;
+    return sum2(s2);
   };
   // B: r' of row t into r and out, and this thread's part of the sum of its squares
-  auto residual = [&](int t, const uint4* st, float i_y) {
-    float2 s2 = both(0.f);
+  auto residual = [&](int t, const uint4* st, float tok) {       // tok = i_y (token gate)
+    f32x2 s2 = both2(0.f);
     if (t >= p.T) return 0.f;
     const size_t base = static_cast<size_t>(t) * p.nvec;
-    float tok = i_y;
-    if (p.gate_kind == MOE_GATE_TOKEN) tok *= load1(p.gate, t, p.w_f32);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
@@ -238,7 +228,7 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
       if (kStaged) r[j] = row8<RES32, kStaged>(st, j, threads, p.r, base + v);
       if (p.res_scale != 1.f) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[j].p[e] = mul2(both(p.res_scale), r[j].p[e]);
+        for (int e = 0; e < 4; ++e) r[j].p[e] = mul2(both2(p.res_scale), r[j].p[e]);
       }
       if (p.y) {
         Vec8 y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
@@ -248,19 +238,19 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
           for (int e = 0; e < 4; ++e) y.p[e] = mul2(y.p[e], g.p[e]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[j].p[e] = fma2(mul2(both(tok), y.p[e]), c[j].p[e], r[j].p[e]);
+        for (int e = 0; e < 4; ++e) r[j].p[e] = fma2(mul2(both2(tok), y.p[e]), c[j].p[e], r[j].p[e]);
       }
       if (p.r_out) store8(p.r_out, base + v, RES32, r[j]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s2 = fma2(r[j].p[e], r[j].p[e], s2);
     }
-    return s2.x + s2.y;
+    return sum2(s2);
   };
   // C: h of row t from r
   auto normalised = [&](int t, float ss) {
     if (t >= p.T) return;
     const size_t base = static_cast<size_t>(t) * p.nvec;
-    const float2 i_r = both(rsqrtf(fmaf(ss, p.inv_d, p.eps)));
+    const f32x2 i_r = both2(rsqrtf(fmaf(ss, p.inv_d, p.eps)));
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
@@ -274,22 +264,29 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
         // 16 consecutive threads (a half-warp: tpr is a multiple of 32) hold a 128-value block
         uint32_t amax = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          amax = max(amax, max(__float_as_uint(fabsf(h.p[e].x)), __float_as_uint(fabsf(h.p[e].y))));
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack2(h.p[e]);
+          amax = max(amax, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
+        }
         amax = __reduce_max_sync((threadIdx.x & 16) ? 0xFFFF0000u : 0x0000FFFFu, amax);
         const int ex = e4m3_scale_exponent(amax);
         uint2 q;
         uint16_t* qh = reinterpret_cast<uint16_t*>(&q);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          qh[e] = __nv_cvt_float2_to_fp8x2(make_float2(scalbnf(h.p[e].x, -ex), scalbnf(h.p[e].y, -ex)),
-                                           __NV_SATFINITE, __NV_E4M3);
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = unpack2(h.p[e]);
+          qh[e] = __nv_cvt_float2_to_fp8x2(make_float2(scalbnf(f.x, -ex), scalbnf(f.y, -ex)), __NV_SATFINITE,
+                                           __NV_E4M3);
+        }
         static_cast<uint2*>(p.h)[base + v] = q;
         if ((v & 15) == 0) p.h_scale[(base + v) >> 4] = ldexpf(1.0f, ex);
       }
     }
   };
   auto i_of = [&](float ss) { return p.w_post ? rsqrtf(fmaf(ss, p.inv_d, p.eps)) : 1.f; };
+  auto token_gate = [&](int t) {
+    return p.gate_kind == MOE_GATE_TOKEN && t < p.T ? load1(p.gate, t, p.w_f32) : 1.f;
+  };
 
   if (!kStaged) {                              // one row per row slot
     const int t = blockIdx.x * p.rows + row;
@@ -298,12 +295,13 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
       for (int j = 0; j < VPT; ++j)
         if (i0 + j * p.tpr < p.nvec) r[j] = load8(p.r, static_cast<size_t>(t) * p.nvec + i0 + j * p.tpr, RES32);
     }
+    const float g = token_gate(t);
     float sy[1] = {0.f};
     if (p.w_post) {
       sy[0] = branch_square(t, nullptr);
       row_sums(sy, part[0], p.tpr);
     }
-    float sr[1] = {residual(t, nullptr, i_of(sy[0]))};
+    float sr[1] = {residual(t, nullptr, i_of(sy[0]) * g)};
     if (!p.w_pre) return;
     row_sums(sr, part[1], p.tpr);
     normalised(t, sr[0]);
@@ -318,11 +316,12 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
   if (p.w_post) row_sums(sums, part[1], p.tpr);
   int turn = 0;
   for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, t += step, ++turn) {
+    const float g = token_gate(t);             // (under way while the rows are waited for)
     fetch(t + (kStages - 1) * step, (turn + kStages - 1) % kRing);
     rows_wait<kStages>();                      // row t + step
     const uint4* st = ring + turn % kRing * stage_vecs + threadIdx.x;
     const uint4* next = ring + (turn + 1) % kRing * stage_vecs + threadIdx.x;
-    sums[0] = residual(t, st, i_of(sums[1]));
+    sums[0] = residual(t, st, i_of(sums[1]) * g);
     if (p.w_post) {
       sums[1] = branch_square(t + step, next);
       row_sums(sums, part[turn & 1], p.tpr);
@@ -379,8 +378,9 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
   auto smem_add = [&](int which, int v, const Vec8& x) {
     float4* s = sums + which * (p.d / 4) + 2 * v;
     const float4 a = s[0], b = s[1];
-    s[0] = make_float4(a.x + x.p[0].x, a.y + x.p[0].y, a.z + x.p[1].x, a.w + x.p[1].y);
-    s[1] = make_float4(b.x + x.p[2].x, b.y + x.p[2].y, b.z + x.p[3].x, b.w + x.p[3].y);
+    const float2 x0 = unpack2(x.p[0]), x1 = unpack2(x.p[1]), x2 = unpack2(x.p[2]), x3 = unpack2(x.p[3]);
+    s[0] = make_float4(a.x + x0.x, a.y + x0.y, a.z + x1.x, a.w + x1.y);
+    s[1] = make_float4(b.x + x2.x, b.y + x2.y, b.z + x3.x, b.w + x3.y);
   };
   // stage: r' and dh (with the pre-norm), dr_out, y, full gate -- in fixed places
   constexpr int kAtDh = VPT * kR, kAtDr = kAtDh + VPT * kY, kAtY = kAtDr + VPT * kR, kAtGate = kAtY + VPT * kY;
@@ -402,7 +402,6 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
         if (p.y) stage_in<ACT32>(st + kAtY * threads, j, threads, p.y, base + v);
         if (full_gate) stage_in<ACT32>(st + kAtGate * threads, j, threads, p.gate, base + v);
       }
-      if (p.gate_kind == MOE_GATE_TOKEN && i0 == 0) prefetch_l1(p.gate, t, p.w_f32);
     }
     rows_commit();
   };
@@ -413,7 +412,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
   auto pre_weight = [&](int v) {
     Vec8 a = load8(p.w_pre, v, p.w_f32);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) a.p[e] = make_float2(a.p[e].x + p.w_offset, a.p[e].y + p.w_offset);
+    for (int e = 0; e < 4; ++e) a.p[e] = add2(a.p[e], both2(p.w_offset));
     return a;
   };
   auto branch_weight = [&](int v) {
@@ -421,7 +420,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
     if (p.w_post) {
       a = load8(p.w_post, v, p.w_f32);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) a.p[e] = make_float2(a.p[e].x + p.w_offset, a.p[e].y + p.w_offset);
+      for (int e = 0; e < 4; ++e) a.p[e] = add2(a.p[e], both2(p.w_offset));
     }
     if (p.gate_kind == MOE_GATE_CHANNEL) {
       const Vec8 g = load8(p.gate, v, p.w_f32);
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
   Vec8 q[VPT];
   // 1: this thread's parts of the sums of r'^2, z r' and y^2 of row t
   auto squares = [&](int t, const uint4* st, float* s) {
-    float2 s0 = both(0.f), s1 = both(0.f), s2 = both(0.f);
+    f32x2 s0 = both2(0.f), s1 = both2(0.f), s2 = both2(0.f);
     const size_t base = static_cast<size_t>(t) * p.nvec;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -467,19 +466,17 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
         for (int e = 0; e < 4; ++e) s2 = fma2(y.p[e], y.p[e], s2);
       }
     }
-    s[0] = s0.x + s0.y;
-    s[1] = s1.x + s1.y;
-    s[2] = s2.x + s2.y;
+    s[0] = sum2(s0);
+    s[1] = sum2(s1);
+    s[2] = sum2(s2);
   };
   // 2: G of row t (dr, the channel sums), q kept, and the parts of the sums of q y and G u
-  auto gradients = [&](int t, const uint4* st, float i_r, float zr, float i_y, float* m) {
+  auto gradients = [&](int t, const uint4* st, float tok, float i_r, float zr, float i_y, float* m) {
     m[0] = m[1] = 0.f;
     if (t >= p.T) return;
     const size_t base = static_cast<size_t>(t) * p.nvec;
-    const float2 k_r = both(-i_r * i_r * i_r * (zr * p.inv_d));
-    float tok = p.branch_scale;
-    if (p.gate_kind == MOE_GATE_TOKEN) tok *= load1(p.gate, t, p.w_f32);
-    float2 m0 = both(0.f), m1 = both(0.f);
+    const f32x2 k_r = both2(-i_r * i_r * i_r * (zr * p.inv_d));
+    f32x2 m0 = both2(0.f), m1 = both2(0.f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
@@ -493,7 +490,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
         Vec8 zx;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 zi = mul2(z.p[e], both(i_r));
+          const f32x2 zi = mul2(z.p[e], both2(i_r));
           if (!kSmem) A[kSmem ? 0 : j].p[e] = fma2(zi, x.p[e], A[kSmem ? 0 : j].p[e]);
           else zx.p[e] = mul2(zi, x.p[e]);
           G.p[e] = fma2(zi, wj.p[e], fma2(k_r, x.p[e], G.p[e]));
@@ -506,7 +503,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
       if (p.res_scale != 1.f) {
         Vec8 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o.p[e] = mul2(both(p.res_scale), G.p[e]);
+        for (int e = 0; e < 4; ++e) o.p[e] = mul2(both2(p.res_scale), G.p[e]);
         store8(p.dr, base + v, RES32, o);
       } else {
         store8(p.dr, base + v, RES32, G);
@@ -516,8 +513,8 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
       Vec8 b;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 n = mul2(y.p[e], both(i_y));                // normalised branch
-        float2 dn = mul2(both(tok), G.p[e]);
+        const f32x2 n = mul2(y.p[e], both2(i_y));                // normalised branch
+        f32x2 dn = mul2(both2(tok), G.p[e]);
         if (full_gate) dn = mul2(dn, g.p[e]);
         q[j].p[e] = mul2(dn, cj.p[e]);                           // q (dy itself without w_post)
         m0 = fma2(q[j].p[e], y.p[e], m0);
@@ -529,21 +526,21 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
         Vec8 dg;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 u = mul2(mul2(both(p.branch_scale), cj.p[e]), mul2(y.p[e], both(i_y)));
+          const f32x2 u = mul2(mul2(both2(p.branch_scale), cj.p[e]), mul2(y.p[e], both2(i_y)));
           dg.p[e] = mul2(G.p[e], u);
           m1 = fma2(G.p[e], u, m1);
         }
         if (full_gate) store8(p.dgate, base + v, ACT32, dg);
       }
     }
-    m[0] = m0.x + m0.y;
-    m[1] = m1.x + m1.y;
+    m[0] = sum2(m0);
+    m[1] = sum2(m1);
   };
   // 3: dy of row t
   auto branch_gradient = [&](int t, const uint4* st, float i_y, float qy, float gu) {
     if (t >= p.T || !p.y) return;
     const size_t base = static_cast<size_t>(t) * p.nvec;
-    const float2 k_y = both(-i_y * i_y * i_y * (qy * p.inv_d));
+    const f32x2 k_y = both2(-i_y * i_y * i_y * (qy * p.inv_d));
     if (i0 == 0 && p.want_gate && p.gate_kind == MOE_GATE_TOKEN) static_cast<float*>(p.dgate)[t] = gu;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -552,7 +549,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
       if (p.w_post) {
         const Vec8 y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q[j].p[e] = fma2(both(i_y), q[j].p[e], mul2(k_y, y.p[e]));
+        for (int e = 0; e < 4; ++e) q[j].p[e] = fma2(both2(i_y), q[j].p[e], mul2(k_y, y.p[e]));
       }
       store8(p.dy, base + v, ACT32, q[j]);
     }
@@ -566,7 +563,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
       squares(t, nullptr, s);
       row_sums(s, part[0], p.tpr);
       const float i_y = p.w_post ? i_of(s[2]) : 1.f;
-      gradients(t, nullptr, i_of(s[0]), s[1], i_y, m);
+      gradients(t, nullptr, scale_of(t), i_of(s[0]), s[1], i_y, m);
       row_sums(m, part[1], p.tpr);
       branch_gradient(t, nullptr, i_y, m[0], m[1]);
     }
@@ -584,11 +581,12 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
     }
     int turn = 0;
     for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, t += step, ++turn) {
+      const float tok = scale_of(t);
       fetch(t + (kStages - 1) * step, (turn + kStages - 1) % kRing);
       rows_wait<kStages>();                    // row t + step
       const uint4* st = ring + turn % kRing * stage_vecs + threadIdx.x;
       const float i_y = p.w_post ? i_of(s[2]) : 1.f;
-      gradients(t, st, i_of(s[0]), s[1], i_y, s + 3);
+      gradients(t, st, tok, i_of(s[0]), s[1], i_y, s + 3);
       squares(t + step, ring + (turn + 1) % kRing * stage_vecs + threadIdx.x, s);
       row_sums(s, part[turn & 1], p.tpr);
       branch_gradient(t, st, i_y, s[3], s[4]);

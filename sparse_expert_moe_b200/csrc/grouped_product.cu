@@ -1230,9 +1230,9 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
       const int rows = t.rows - sub * 32;        // its rows (<= 0: none)
       const bool here = half < halves();
       const bool mine = here && rows > 0;
-      float acc[128];
+      f32x2 acc[64];                             // 128 sums
 #pragma unroll
-      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      for (int i = 0; i < 64; ++i) acc[i] = both2(0.f);
       const float* sa = p.a_scale + static_cast<size_t>(t.row0 + min(sub * 32 + lane, t.rows - 1)) * p.k_blocks;
       const float* sw = p.w_scale + (static_cast<size_t>(t.g) * p.w_scale_rows +
                                      min(2 * t.mb + half, p.w_scale_rows - 1)) * p.k_blocks;
@@ -1259,15 +1259,15 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
         if (mine) {
           const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
           const float g = kq == 0 ? f[0] : (kq == 1 ? f[1] : (kq == 2 ? f[2] : f[3]));
-          const float2 gg = make_float2(g, g);
+          const f32x2 gg = both2(g);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float v[32];
             tmem_ld32(tb + q * 32, v);
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              float2* a = reinterpret_cast<float2*>(&acc[q * 32 + i]);
-              *a = fma2(gg, make_float2(v[i], v[i + 1]), *a);
+              f32x2& a = acc[(q * 32 + i) / 2];
+              a = fma2(gg, pack2(v[i], v[i + 1]), a);
             }
           }
           tc_fence_before();
@@ -1281,9 +1281,21 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
           store_direct<OUT>(static_cast<OUT*>(p.out) + static_cast<size_t>(t.row0 + sub * 32) * p.ld_out + col0 + i,
                             p.ld_out, rows, p.m_total - col0 - i, v, stg, lane);
       };
+      auto sixteen = [&](int i, float* v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 f = unpack2(acc[i / 2 + e]);
+          v[2 * e] = f.x;
+          v[2 * e + 1] = f.y;
+        }
+      };
       if (!sched.cut(c)) {
 #pragma unroll
-        for (int i = 0; i < 128; i += 16) finish(acc + i, i);
+        for (int i = 0; i < 128; i += 16) {
+          float v[16];
+          sixteen(i, v);
+          finish(v, i);
+        }
         continue;
       }
       int first, last;
@@ -1292,7 +1304,12 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
       if (mine) {
         float* to = slot(blockIdx.x);
 #pragma unroll
-        for (int i = 0; i < 128; i += 4) write_part(to, half * 128 + i, acc + i);
+        for (int i = 0; i < 128; i += 16) {
+          float v[16];
+          sixteen(i, v);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) write_part(to, half * 128 + i + e, v + e);
+        }
       }
       if (!arrive_last(p.header, first, last - first + 1, sync, last_flag, warp == 4 && lane == 0, lane, ok)) continue;
       for (int i = 0; i < 128 && mine; i += 32) {
