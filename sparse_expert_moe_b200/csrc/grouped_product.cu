@@ -331,9 +331,9 @@ struct EpilogueSync {
   __device__ __forceinline__ bool operator()(int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    const bool ok = mbar_wait(bar, parity, abort_flag, status);
+    const bool ok = mbar_wait_warp(bar, parity, abort_flag, status);
     parity ^= 1u;
-    return __all_sync(0xffffffffu, ok) != 0;
+    return ok;
   }
 };
 
@@ -559,11 +559,8 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
         const Tile t = token_tile(gt, c.tile, C::kNTok, 16, m_blocks, 1);
         const float* sa = p.a_scale + static_cast<size_t>(t.row0 + min(lane, t.rows - 1)) * p.k_blocks;
         for (int kb = c.kb0; kb < c.kb1; kb += kScaleBlocks, ++it) {
-          const bool w = mbar_wait(&sempty_bar[it & 1], ((it >> 1) & 1u) ^ 1u, abort_flag, status);
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
-          }
+          ok = mbar_wait_warp(&sempty_bar[it & 1], ((it >> 1) & 1u) ^ 1u, abort_flag, status);
+          if (!ok) break;
           float* dst = scales + (it & 1) * (kScaleBlocks * C::kMB * C::kNTok);
           float s[kScaleBlocks], ws[C::kMB][kScaleBlocks];
 #pragma unroll
@@ -604,13 +601,9 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
         for (int kb = c.kb0; kb < c.kb1; ++kb, ++it) {
           const uint32_t b = it % C::kBufs;
           const int q = (kb - c.kb0) % kScaleBlocks;
-          bool w = true;
-          if (q == 0) w = mbar_wait(&sfull_bar[sit & 1], (sit >> 1) & 1u, abort_flag, status);
-          w = w && mbar_wait(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
-          }
+          ok = (q != 0 || mbar_wait_warp(&sfull_bar[sit & 1], (sit >> 1) & 1u, abort_flag, status)) &&
+               mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
           const float* sc = scales + ((sit & 1) * kScaleBlocks + q) * (C::kMB * C::kNTok);
@@ -636,8 +629,7 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
         if (!ok) break;
       } else {
         const uint32_t b = it % C::kBufs;
-        const bool w = mbar_wait(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
-        if (!__all_sync(0xffffffffu, w)) break;
+        if (!mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status)) break;
         tc_fence_after();
         const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
 #pragma unroll
@@ -903,11 +895,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
         const int boxes = 2 + grad_n() / 128;
         for (int kb = c.kb0; kb < c.kb1; ++kb, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
           if (!ragged_block(t.rows, kb)) continue;
-          const bool w = mbar_wait(&land_bar[stage], (parity >> stage) & 1u, abort_flag, status);
-          if (!__all_sync(0xffffffffu, w)) {
-            ok = false;
-            break;
-          }
+          ok = mbar_wait_warp(&land_bar[stage], (parity >> stage) & 1u, abort_flag, status);
+          if (!ok) break;
           parity ^= 1u << stage;
           const int left = t.rows - kb * 64;
           uint8_t* st = tiles + stage * C::kStage;
@@ -973,8 +962,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
         uint32_t tb = 0;
         if (rows) {
           const uint32_t b = it % C::kBufs;
-          const bool w = mbar_wait(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
-          if (!__all_sync(0xffffffffu, w)) break;
+          if (!mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status)) break;
           tc_fence_after();
           tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
         }
@@ -1017,8 +1005,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
         }
       } else {
         const uint32_t b = it % C::kBufs;
-        const bool w = mbar_wait(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
-        if (!__all_sync(0xffffffffu, w)) break;
+        if (!mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status)) break;
         tc_fence_after();
         const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
         for (int n0 = 0; n0 < cols; n0 += 16) {

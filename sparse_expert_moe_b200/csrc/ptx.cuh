@@ -134,10 +134,36 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return mbar_wait_budget(bar, parity, abort_flag, status, kWaitBudgetCycles);
 }
 
-// The same for a whole warp: the answer is one for all of its lanes.
+// A wait for a whole warp: the answer is one for all of its lanes.  Each try may suspend the warp
+// for some microseconds, so that a long wait (an epilogue's for a tile) does not spend issue slots
+// and power on polling.
+__device__ __forceinline__ bool mbar_try_wait_suspended(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(16384u)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                int* status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
+  const uint32_t a = smem_u32(bar);
+  bool ok = mbar_try_wait_suspended(a, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    const long long t0 = clock64();
+    while (!(ok = mbar_try_wait_suspended(a, parity))) {
+      if (*abort_flag) break;
+      if (clock64() - t0 > kWaitBudgetCycles) {
+        record_status(status, kStatusTimeout);
+        *abort_flag = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
 }
 
 // One lane of a converged warp, always the same.  Code around it stays warp-uniform, so that the
