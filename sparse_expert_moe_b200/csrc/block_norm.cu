@@ -555,6 +555,9 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
     }
   };
   auto i_of = [&](float ss) { return rsqrtf(fmaf(ss, p.inv_d, p.eps)); };
+  auto scale_of = [&](int t) {                 // branch_scale (token gate)
+    return p.gate_kind == MOE_GATE_TOKEN && t < p.T ? p.branch_scale * load1(p.gate, t, p.w_f32) : p.branch_scale;
+  };
   int t = blockIdx.x * p.rows + row;
   if (!kStaged) {
     // every thread of the CTA makes the same number of turns (row_sums synchronises it)

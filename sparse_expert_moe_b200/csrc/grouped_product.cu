@@ -292,34 +292,37 @@ __device__ __forceinline__ void store_transposed(T* out, size_t ld, int rows, in
     __syncwarp();
   }
 }
-// A warp's 32 rows (lane = row) x 16 columns to rows of `out`, likewise.
+// A warp's 32 rows (lane = row) x 16 columns to rows of `out`, likewise; 32 bytes of a row at a
+// time through 1 KB.
 template <typename T>
 __device__ __forceinline__ void store_direct(T* out, size_t ld, int rows, int cols, const float* v,
                                              void* stage_raw, int lane) {
-  constexpr int kElems = 16 / static_cast<int>(sizeof(T)), kVecs = 16 / kElems;   // 16-byte units per row
+  constexpr int kElems = 16 / static_cast<int>(sizeof(T));         // per 16-byte unit
   uint4* stage = static_cast<uint4*>(stage_raw);
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    uint4 q;
-    if constexpr (sizeof(T) == 4) {
-      q = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]),
-                     __float_as_uint(v[4 * u + 3]));
-    } else {
-      __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&q);
+  for (int c0 = 0; c0 < 16; c0 += 2 * kElems) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) b[e] = __floats2bfloat162_rn(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]);
+    for (int u = 0; u < 2; ++u) {
+      const float* x = v + c0 + u * kElems;
+      uint4 q;
+      if constexpr (sizeof(T) == 4) {
+        q = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+      } else {
+        __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[e] = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+      }
+      stage[lane * 2 + (u ^ ((lane >> 2) & 1))] = q;               // spread over the banks
     }
-    stage[lane * kVecs + (u ^ ((lane * kVecs / 8) & (kVecs - 1)))] = q;   // spread over the banks
-  }
-  __syncwarp();
+    __syncwarp();
 #pragma unroll
-  for (int i = lane; i < 32 * kVecs; i += 32) {
-    const int r = i / kVecs, u = i % kVecs;
-    if (r < rows && u * kElems < cols)
-      *reinterpret_cast<uint4*>(out + r * ld + u * kElems) =
-          stage[r * kVecs + (u ^ ((r * kVecs / 8) & (kVecs - 1)))];
+    for (int i = lane; i < 64; i += 32) {
+      const int r = i >> 1, u = i & 1;
+      if (r < rows && c0 + u * kElems < cols)
+        *reinterpret_cast<uint4*>(out + r * ld + c0 + u * kElems) = stage[r * 2 + (u ^ ((r >> 2) & 1))];
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 // Barrier between the epilogue warps of a CTA, bounded like every other wait.
@@ -331,7 +334,7 @@ struct EpilogueSync {
   __device__ __forceinline__ bool operator()(int lane) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    const bool ok = mbar_wait_warp(bar, parity, abort_flag, status);
+    const bool ok = mbar_poll_warp(bar, parity, abort_flag, status);
     parity ^= 1u;
     return ok;
   }
@@ -476,7 +479,7 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
       const int box = t.rows > 16 ? 32 : 16;
       const CUtensorMap* tm = &p.tmap[box == 32 ? 2 : 3];
       for (int kb = c.kb0; kb < c.kb1; ++kb) {
-        ok = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
+        ok = mbar_poll_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
         if (!ok) break;
         uint8_t* st = tiles + stage * C::kStage;
         uint64_t* bar = &full_bar[stage];
@@ -516,12 +519,12 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
       for (int kb = c.kb0; kb < c.kb1; ++kb) {
         if (F8 || kb == c.kb0) {                // a fresh accumulator buffer
           b = it % C::kBufs;
-          ok = mbar_wait_warp(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status);
+          ok = mbar_poll_warp(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status);
           if (!ok) break;
           d0 = tmem + b * C::kCols;
           ++it;
         }
-        ok = mbar_wait_warp(&full_bar[stage], phase, abort_flag, status);
+        ok = mbar_poll_warp(&full_bar[stage], phase, abort_flag, status);
         if (!ok) break;
         tc_fence_after();
         const uint32_t sa = smem_u32(tiles) + stage * C::kStage, sb = sa + C::kA;
@@ -559,7 +562,7 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
         const Tile t = token_tile(gt, c.tile, C::kNTok, 16, m_blocks, 1);
         const float* sa = p.a_scale + static_cast<size_t>(t.row0 + min(lane, t.rows - 1)) * p.k_blocks;
         for (int kb = c.kb0; kb < c.kb1; kb += kScaleBlocks, ++it) {
-          ok = mbar_wait_warp(&sempty_bar[it & 1], ((it >> 1) & 1u) ^ 1u, abort_flag, status);
+          ok = mbar_poll_warp(&sempty_bar[it & 1], ((it >> 1) & 1u) ^ 1u, abort_flag, status);
           if (!ok) break;
           float* dst = scales + (it & 1) * (kScaleBlocks * C::kMB * C::kNTok);
           float s[kScaleBlocks], ws[C::kMB][kScaleBlocks];
@@ -601,8 +604,8 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
         for (int kb = c.kb0; kb < c.kb1; ++kb, ++it) {
           const uint32_t b = it % C::kBufs;
           const int q = (kb - c.kb0) % kScaleBlocks;
-          ok = (q != 0 || mbar_wait_warp(&sfull_bar[sit & 1], (sit >> 1) & 1u, abort_flag, status)) &&
-               mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
+          ok = (q != 0 || mbar_poll_warp(&sfull_bar[sit & 1], (sit >> 1) & 1u, abort_flag, status)) &&
+               mbar_poll_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
           if (!ok) break;
           tc_fence_after();
           const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
@@ -784,7 +787,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
     while (ok && fetch()) {
       const int m0 = t.mb * 256 + rank * 128;
       for (int kb = c.kb0; kb < c.kb1; ++kb) {
-        ok = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
+        ok = mbar_poll_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
         if (!ok) break;
         uint8_t* st = tiles + stage * C::kStage;
         uint8_t* bt = st + kTileA;
@@ -849,7 +852,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
       while (ok && fetch()) {
         if (c.kb1 <= c.kb0) continue;                             // TN: a group without rows
         const uint32_t b = it % C::kBufs;
-        if (!mbar_wait_warp(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status)) break;
+        if (!mbar_poll_warp(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status)) break;
         ++it;
         const int n_pad = OP == kTN ? grad_n() : (t.rows + 31) & ~31;
         const uint32_t idesc = idesc_bf16_f32(256, n_pad) | (OP != kNT ? kIdescAMajorMN : 0u) |
@@ -858,7 +861,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
         for (int kb = c.kb0; kb < c.kb1; ++kb) {
           ok = OP == kTN && ragged_block(t.rows, kb)
                    ? __all_sync(0xffffffffu, mbar_wait_cluster(&full_bar[stage], phase, abort_flag, status)) != 0
-                   : mbar_wait_warp(&full_bar[stage], phase, abort_flag, status);
+                   : mbar_poll_warp(&full_bar[stage], phase, abort_flag, status);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sa = smem_u32(tiles) + stage * C::kStage, sb = sa + kTileA;
@@ -895,7 +898,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
         const int boxes = 2 + grad_n() / 128;
         for (int kb = c.kb0; kb < c.kb1; ++kb, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
           if (!ragged_block(t.rows, kb)) continue;
-          ok = mbar_wait_warp(&land_bar[stage], (parity >> stage) & 1u, abort_flag, status);
+          ok = mbar_poll_warp(&land_bar[stage], (parity >> stage) & 1u, abort_flag, status);
           if (!ok) break;
           parity ^= 1u << stage;
           const int left = t.rows - kb * 64;
@@ -1047,7 +1050,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
 // column to column; reading 128 factors per thread and K block from shared memory took 1024 of
 // 2100 cycles, 446 us at T = 8192, n = 4096, k = 7168.)  The tile's columns are two halves of
 // 128, one 128-row weight block each, with two TMEM buffers of 128 columns; four epilogue warps
-// fold either half, 128 fp32 sums per thread, while the other buffer is written.
+// fold either half, 128 fp32 sums per thread, while the other buffer is written.  (Eight warps per
+// half with 64 sums each measured 365 us there against 312: twice the waits and arrivals.)
 struct FoldCfg {
   static constexpr int kWidth = 128;                              // tokens
   static constexpr uint32_t kStage = 3 * kTileA;                  // 128 token + 256 weight rows: 48 KB
@@ -1129,7 +1133,7 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
       while (ok && fetch()) {
         const int n_pad = (t.rows + 15) & ~15, nh = halves();
         for (int kb = c.kb0; kb < c.kb1; ++kb) {
-          ok = mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
+          ok = mbar_poll_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
           if (!ok) break;
           uint8_t* st = tiles + stage * C::kStage;
           uint64_t* bar = &full_bar[stage];
@@ -1165,8 +1169,8 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
         const int nh = halves();
         for (int kb = c.kb0; kb < c.kb1; ++kb) {
           const uint32_t b0 = it0 & 1u, b1 = 2u + (it1 & 1u);
-          ok = mbar_wait_warp(&full_bar[stage], phase, abort_flag, status) &&
-               mbar_wait_warp(&tempty_bar[b0], ((it0 >> 1) & 1u) ^ 1u, abort_flag, status);
+          ok = mbar_poll_warp(&full_bar[stage], phase, abort_flag, status) &&
+               mbar_poll_warp(&tempty_bar[b0], ((it0 >> 1) & 1u) ^ 1u, abort_flag, status);
           if (!ok) break;
           ++it0;
           tc_fence_after();
@@ -1181,7 +1185,7 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
           }
           __syncwarp();
           if (nh > 1) {
-            ok = mbar_wait_warp(&tempty_bar[b1], ((it1 >> 1) & 1u) ^ 1u, abort_flag, status);
+            ok = mbar_poll_warp(&tempty_bar[b1], ((it1 >> 1) & 1u) ^ 1u, abort_flag, status);
             if (!ok) break;
             ++it1;
             tc_fence_after();
@@ -1240,7 +1244,7 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
           if (kb + kRun < c.kb1) scales(kb + kRun);
         }
         const uint32_t b = 2 * half + (it & 1u);
-        ok = mbar_wait_warp(&tfull_bar[b], (it >> 1) & 1u, abort_flag, status);
+        ok = mbar_poll_warp(&tfull_bar[b], (it >> 1) & 1u, abort_flag, status);
         if (!ok) break;
         tc_fence_after();
         if (mine) {

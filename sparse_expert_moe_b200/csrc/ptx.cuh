@@ -166,6 +166,12 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, v
   return __all_sync(0xffffffffu, ok) != 0;
 }
 
+// The same without the suspension, for waits of a fraction of a microsecond.
+__device__ __forceinline__ bool mbar_poll_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                               int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status)) != 0;
+}
+
 // One lane of a converged warp, always the same.  Code around it stays warp-uniform, so that the
 // operands of TMA and tcgen05 instructions are computed in uniform registers; inside a branch on
 // the lane number each operand is moved there again for every instruction.
