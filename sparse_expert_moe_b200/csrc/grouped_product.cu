@@ -186,16 +186,26 @@ struct Piece {
   int tile, kb0, kb1;
 };
 
-// Stream kernel: the K blocks of all tiles as one sequence, cut into `sharers` equal pieces.
+// Stream kernel: the K blocks of all tiles as one sequence, cut into equal pieces, one per CTA --
+// or, where there are fewer than half as many tiles as CTAs, every tile cut into the same number
+// of parts, one per CTA, so that no CTA has to join two tiles.  Two K blocks at least either way.
 struct EvenShare {
-  int kb, sharers;
+  int kb, sharers, parts;       // parts > 0: of every tile
   long long total, u, u1;
 
   __device__ __forceinline__ EvenShare(int me, int n, int n_tiles, int kb_) : kb(kb_) {
     total = static_cast<long long>(n_tiles) * kb;
-    sharers = (total + 1) / 2 < n ? static_cast<int>((total + 1) / 2) : n;   // two K blocks at least
+    sharers = (total + 1) / 2 < n ? static_cast<int>((total + 1) / 2) : n;
+    parts = 0;
     u = u1 = 0;
-    if (me < sharers) {
+    if (n_tiles > 0 && 2 * n_tiles <= n) {
+      parts = max(1, min(n / n_tiles, kb / 2));
+      if (me < n_tiles * parts) {
+        const long long b = static_cast<long long>(me / parts) * kb;
+        u = b + kb * (me % parts) / parts;
+        u1 = b + kb * (me % parts + 1) / parts;
+      }
+    } else if (me < sharers) {
       u = total * me / sharers;
       u1 = total * (me + 1) / sharers;
     }
@@ -216,9 +226,14 @@ struct EvenShare {
     return static_cast<int>(((unit + 1) * sharers - 1) / total);
   }
   __device__ __forceinline__ void owners(int t, int& first, int& last) const {
-    const long long b = static_cast<long long>(t) * kb;
-    first = owner(b);
-    last = owner(b + kb - 1);
+    if (parts) {
+      first = t * parts;
+      last = first + parts - 1;
+    } else {
+      const long long b = static_cast<long long>(t) * kb;
+      first = owner(b);
+      last = owner(b + kb - 1);
+    }
   }
 };
 
