@@ -328,7 +328,8 @@ MOE_API moe_status moe_norm_workspace_size(const moe_norm_config *cfg, size_t *b
  *   r_out  NULL: not stored
  *   h_scale [T, d/128] fp32 when cfg->out is MOE_E4M3, else NULL
  * r_out may be r itself; h may be y or r itself where the types have one size.  Tensors
- * 16-byte aligned (a token gate and h_scale: by their element). */
+ * 16-byte aligned (a token gate and h_scale: by their element).  T = 0 does nothing.  Neither
+ * call records a device status. */
 MOE_API moe_status moe_block_norm(const moe_norm_config *cfg, const void *r, const void *y,
                                   const void *w_post, const void *gate, const void *w_pre, void *r_out,
                                   void *h, float *h_scale, cudaStream_t stream);
@@ -359,7 +360,10 @@ MOE_API moe_status moe_block_norm_backward(const moe_norm_config *cfg, const voi
  *   in   MOE_BF16 (n and k multiples of 8) or MOE_E4M3_FP32_SCALE (n % 8 == 0, k % 16 == 0;
  *        moe_grouped_gemm only)
  *   out  MOE_BF16 or MOE_F32
- * 1 <= n_groups <= 1024; n, k <= 65536. */
+ * 1 <= n_groups <= 1024; n, k <= 65536; n_rows <= 2^24.
+ * Calls that share a workspace must not overlap on the GPU.  Tiles that several CTAs sum up
+ * are joined in a fixed order: reruns are bit-identical.  After MOE_ERR_TIMEOUT the header must
+ * be reset (moe_reset_device_status) before the workspace is used again. */
 typedef struct {
   int32_t n_groups, n_rows, n, k;
   moe_dtype in, out;

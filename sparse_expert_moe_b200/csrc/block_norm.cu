@@ -768,11 +768,10 @@ moe_status moe_block_norm(const moe_norm_config* cfg, const void* r, const void*
                           cudaStream_t stream) {
   const moe_status st = check_norm(cfg);
   if (st != MOE_OK) return st;
+  if (cfg->T == 0) return MOE_OK;                // (tensors of no rows have no address to check)
   if ((cfg->gate != MOE_GATE_NONE) != (gate != nullptr) || (!y && (w_post || gate)) || !w_pre != !h ||
-      (h && (cfg->out == MOE_E4M3) != (h_scale != nullptr)) || (!h && h_scale) || (!r_out && !h))
+      (h && (cfg->out == MOE_E4M3) != (h_scale != nullptr)) || (!h && h_scale) || (!r_out && !h) || !r)
     return MOE_ERR_INVALID_ARG;
-  if (cfg->T == 0) return MOE_OK;
-  if (!r) return MOE_ERR_INVALID_ARG;
   if (unaligned16(r) || unaligned16(y) || unaligned16(w_post) || unaligned16(w_pre) || unaligned16(r_out) ||
       unaligned16(h) || (cfg->gate != MOE_GATE_TOKEN && unaligned16(gate)))
     return MOE_ERR_INVALID_ARG;
@@ -806,9 +805,11 @@ moe_status moe_block_norm_backward(const moe_norm_config* cfg, const void* r_out
                                    cudaStream_t stream) {
   const moe_status st = check_norm(cfg);
   if (st != MOE_OK) return st;
-  if ((cfg->gate != MOE_GATE_NONE) != (gate != nullptr) || (!y && (w_post || gate)) || !w_pre != !dh ||
-      !y != !dy || (dgate && !gate) || (dw_post && !w_post) || (dw_pre && !w_pre) || !ws || !dr ||
-      (w_pre && !r_out) || (!dh && !dr_out))
+  if (!ws || (dgate && cfg->gate == MOE_GATE_NONE) || (dw_post && !w_post) || (dw_pre && !w_pre))
+    return MOE_ERR_INVALID_ARG;
+  if (cfg->T > 0 &&                              // (tensors of no rows have no address to check)
+      ((cfg->gate != MOE_GATE_NONE) != (gate != nullptr) || (!y && (w_post || gate)) || !w_pre != !dh || !y != !dy ||
+       !dr || (w_pre && !r_out) || (!dh && !dr_out)))
     return MOE_ERR_INVALID_ARG;
   if (unaligned16(r_out) || unaligned16(y) || unaligned16(w_post) || unaligned16(w_pre) || unaligned16(dh) ||
       unaligned16(dr_out) || unaligned16(dr) || unaligned16(dy) || unaligned16(ws) || unaligned16(dw_post) ||

@@ -31,6 +31,8 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -1343,12 +1345,13 @@ size_t product_workspace() {
 }
 
 int device_sms() {
-  static int cached[64] = {};
+  static std::atomic<int> cached[64];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64 && cached[dev]) return cached[dev];
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && (n = cached[dev].load(std::memory_order_relaxed))) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-  if (dev >= 0 && dev < 64) cached[dev] = n;
+  if (keep) cached[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -68,8 +68,13 @@ def test_norm_unknown_gate(lib):
 
 
 def test_norm_of_no_tokens_is_a_no_op(lib):
-    fn, *args = norm_call(cfg=dict(T=0), r=None)
-    fn(*args, stream=0)
+    """Tensors without rows have null addresses: nothing about them is refused."""
+    none = dict(r=None, y=None, r_out=None, h=None)
+    for kw in (dict(cfg=dict(T=0), r=None), dict(cfg=dict(T=0), **none),
+               dict(cfg=dict(T=0, out="e4m3"), h_scale=None, **none),
+               dict(cfg=dict(T=0, gate="full"), **none)):
+        fn, *args = norm_call(**kw)
+        fn(*args, stream=0)
 
 
 BWD = ("r_out", "y", "w_post", "gate", "w_pre", "dh", "dr_out", "dr", "dy", "dgate", "dw_post", "dw_pre")
