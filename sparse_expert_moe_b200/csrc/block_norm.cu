@@ -81,8 +81,14 @@ __device__ __forceinline__ float load1(const void* base, size_t i, bool f32) {
              : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
 }
 
+// load1 in two halves: the bits, wanted a turn later, and their value.
+__device__ __forceinline__ uint32_t load1_bits(const void* base, size_t i, bool f32) {
+  return f32 ? __ldg(static_cast<const uint32_t*>(base) + i) : __ldg(static_cast<const unsigned short*>(base) + i);
+}
+__device__ __forceinline__ float value1(uint32_t bits, bool f32) { return __uint_as_float(f32 ? bits : bits << 16); }
+
 // Sums of N values over the threads of a row, the same in every thread of it and in the same
-// order every time.  `part`: shared memory, N floats per warp of the CTA, not touched since
+// order every time.  `part`: shared memory, 32 N floats, not touched since
 // the __syncthreads before the call before last.  All threads of the CTA call this.
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float* part, int tpr) {
@@ -96,13 +102,25 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* part, int tpr) {
   const int first = warp / warps * warps;
   if (lane == 0)
 #pragma unroll
-    for (int j = 0; j < N; ++j) part[warp * N + j] = v[j];
+    for (int j = 0; j < N; ++j) part[j * 32 + warp] = v[j];
   __syncthreads();
+  if (warps <= 16) {                           // two values at a time, 16 lanes each
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    v[j] = lane < warps ? part[(first + lane) * N + j] : 0.f;
+    for (int j = 0; j < N; j += 2) {
+      const int at = j + (lane >> 4), w = lane & 15;
+      float x = w < warps && at < N ? part[at * 32 + first + w] : 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+      for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      v[j] = __shfl_sync(0xffffffffu, x, 0);
+      if (j + 1 < N) v[j + 1] = __shfl_sync(0xffffffffu, x, 16);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      v[j] = lane < warps ? part[j * 32 + first + lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+    }
   }
 }
 
@@ -116,23 +134,24 @@ __device__ __forceinline__ void rows_wait() {   // all but the newest kStages - 
 }
 __device__ __forceinline__ void rows_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
-// One array's vectors of a thread in one stage: 16 or 32 bytes each, thread-interleaved.
-template <bool F32>
-__device__ __forceinline__ void stage_in(uint4* st, int slot, int threads, const void* base, size_t v) {
+// One array's vectors of a thread in one stage: 16 or 32 bytes each, thread-interleaved, kPitch
+// threads apart (a constant, so that the places are immediate offsets).
+template <bool F32, int kPitch>
+__device__ __forceinline__ void stage_in(uint4* st, int slot, const void* base, size_t v) {
   const uint4* g = static_cast<const uint4*>(base);
   if (F32) {
-    cp_async_16_cg(st + (2 * slot) * threads, g + 2 * v);
-    cp_async_16_cg(st + (2 * slot + 1) * threads, g + 2 * v + 1);
+    cp_async_16_cg(st + (2 * slot) * kPitch, g + 2 * v);
+    cp_async_16_cg(st + (2 * slot + 1) * kPitch, g + 2 * v + 1);
   } else {
-    cp_async_16_cg(st + slot * threads, g + v);
+    cp_async_16_cg(st + slot * kPitch, g + v);
   }
 }
-// Vector `slot` of this thread: from its stage, or straight from the array.
-template <bool F32, bool STAGED>
-__device__ __forceinline__ Vec8 row8(const uint4* st, int slot, int threads, const void* base, size_t v) {
-  if (!STAGED) return load8(base, v, F32);
-  if (F32) return unpack_f32(st[2 * slot * threads], st[(2 * slot + 1) * threads]);
-  return unpack_bf16(st[slot * threads]);
+// Vector `slot` of this thread: from its stage, or (kPitch 0) straight from the array.
+template <bool F32, int kPitch>
+__device__ __forceinline__ Vec8 row8(const uint4* st, int slot, const void* base, size_t v) {
+  if (!kPitch) return load8(base, v, F32);
+  if (F32) return unpack_f32(st[2 * slot * kPitch], st[(2 * slot + 1) * kPitch]);
+  return unpack_bf16(st[slot * kPitch]);
 }
 
 // Thread i of a row holds vectors i, i + tpr, ...; a CTA walks rows blockIdx.x * rows + row,
@@ -140,24 +159,27 @@ __device__ __forceinline__ Vec8 row8(const uint4* st, int slot, int threads, con
 // into registers: c = branch_scale (w_post + o) (channel gate), and w_pre + o.
 //
 // Bound by HBM where rows are many.  Measured at T = 8192, d = 7168, bf16, post-norm, token gate
-// and pre-norm (470 MB): one row per CTA, scalar arithmetic, weights fetched per row 172 us
-// (2.7 TB/s); staged 134 us, with 50 instructions per element issued 57% of the time; the
-// present form is given at its launch.
-template <bool RES32, bool ACT32, int VPT, int kStages>
-__global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 448 : 512),
-                                  kStages > 0 && VPT == 2 ? 2 : 1)
+// and pre-norm (470 MB): 74 us, 6.3 TB/s, 0.97 of the measured copy bandwidth.  On the way there:
+// one row per CTA, weights fetched per row 172 us (a row's loads and its two sums took turns);
+// rows staged 134 us (50 instructions per element, issued 57% of the time); packed arithmetic, the
+// weights in registers, one barrier per row 96 us; no tests per vector, one CTA per SM without
+// spills and the token gate's bits fetched a row ahead 74 us.
+//
+// kAll (staged): a branch with its norm, no full gate, both outputs and no vectors past the row's
+// end -- what a block normally has -- without the tests for it per vector.
+template <bool RES32, bool ACT32, int VPT, int kStages, bool kAll = false>
+__global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 448 : 512), 1)
     block_norm_kernel(const NormArgs p) {
   __shared__ float part[2][64];
   extern __shared__ uint4 ring[];
   constexpr bool kStaged = kStages > 0;
-  constexpr int kRing = kStaged ? kStages : 1;
+  constexpr int kRing = kStaged ? kStages : 1, kPitch = kStaged ? (VPT == 2 ? 448 : 512) : 0;
   constexpr int kAtY = VPT * (RES32 ? 2 : 1), kAtGate = kAtY + VPT * (ACT32 ? 2 : 1);
-  const int threads = blockDim.x;
   const int row = threadIdx.x / p.tpr, i0 = threadIdx.x - row * p.tpr;
   const int step = gridDim.x * p.rows;
-  const bool full_gate = p.gate_kind == MOE_GATE_FULL;
-  const int stage_vecs =
-      (p.y ? kAtGate + (full_gate ? VPT * (ACT32 ? 2 : 1) : 0) : kAtY) * threads;
+  const bool full_gate = !kAll && p.gate_kind == MOE_GATE_FULL;
+  const bool branch = kAll || p.y, post = kAll || p.w_post, pre = kAll || p.w_pre;
+  const int stage_vecs = (branch ? kAtGate + (full_gate ? VPT * (ACT32 ? 2 : 1) : 0) : kAtY) * kPitch;
   auto fetch = [&](int t, int s) {
     if (t < p.T) {
       uint4* st = ring + s * stage_vecs + threadIdx.x;
@@ -165,10 +187,10 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         const int v = i0 + j * p.tpr;
-        if (v >= p.nvec) break;
-        stage_in<RES32>(st, j, threads, p.r, base + v);
-        if (p.y) stage_in<ACT32>(st + kAtY * threads, j, threads, p.y, base + v);
-        if (full_gate) stage_in<ACT32>(st + kAtGate * threads, j, threads, p.gate, base + v);
+        if (!kAll && v >= p.nvec) break;
+        stage_in<RES32, kPitch>(st, j, p.r, base + v);
+        if (branch) stage_in<ACT32, kPitch>(st + kAtY * kPitch, j, p.y, base + v);
+        if (full_gate) stage_in<ACT32, kPitch>(st + kAtGate * kPitch, j, p.gate, base + v);
       }
     }
     rows_commit();
@@ -182,8 +204,8 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
     const int v = i0 + j * p.tpr;
     c[j] = constant8(p.branch_scale);
     w[j] = constant8(0.f);
-    if (v >= p.nvec) continue;
-    if (p.w_post) {
+    if (!kAll && v >= p.nvec) continue;
+    if (post) {
       const Vec8 a = load8(p.w_post, v, p.w_f32);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -194,7 +216,7 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
 #pragma unroll
       for (int e = 0; e < 4; ++e) c[j].p[e] = mul2(c[j].p[e], a.p[e]);
     }
-    if (p.w_pre) {
+    if (pre) {
       w[j] = load8(p.w_pre, v, p.w_f32);
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[j].p[e] = add2(w[j].p[e], both2(p.w_offset));
@@ -209,8 +231,8 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (t >= p.T || v >= p.nvec) continue;
-      const Vec8 y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
+      if (t >= p.T || (!kAll && v >= p.nvec)) continue;
+      const Vec8 y = row8<ACT32, kPitch>(st + kAtY * kPitch, j, p.y, base + v);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s2 = fma2(y.p[e], y.p[e], s2);
     }
@@ -224,23 +246,23 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (v >= p.nvec) continue;
-      if (kStaged) r[j] = row8<RES32, kStaged>(st, j, threads, p.r, base + v);
+      if (!kAll && v >= p.nvec) continue;
+      if (kStaged) r[j] = row8<RES32, kPitch>(st, j, p.r, base + v);
       if (p.res_scale != 1.f) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) r[j].p[e] = mul2(both2(p.res_scale), r[j].p[e]);
       }
-      if (p.y) {
-        Vec8 y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
+      if (branch) {
+        Vec8 y = row8<ACT32, kPitch>(st + kAtY * kPitch, j, p.y, base + v);
         if (full_gate) {
-          const Vec8 g = row8<ACT32, kStaged>(st + kAtGate * threads, j, threads, p.gate, base + v);
+          const Vec8 g = row8<ACT32, kPitch>(st + kAtGate * kPitch, j, p.gate, base + v);
 #pragma unroll
           for (int e = 0; e < 4; ++e) y.p[e] = mul2(y.p[e], g.p[e]);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) r[j].p[e] = fma2(mul2(both2(tok), y.p[e]), c[j].p[e], r[j].p[e]);
       }
-      if (p.r_out) store8(p.r_out, base + v, RES32, r[j]);
+      if (kAll || p.r_out) store8(p.r_out, base + v, RES32, r[j]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) s2 = fma2(r[j].p[e], r[j].p[e], s2);
     }
@@ -254,7 +276,7 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (v >= p.nvec) continue;               // for e4m3: whole half-warps at a time
+      if (!kAll && v >= p.nvec) continue;               // for e4m3: whole half-warps at a time
       Vec8 h;
 #pragma unroll
       for (int e = 0; e < 4; ++e) h.p[e] = mul2(mul2(r[j].p[e], i_r), w[j].p[e]);
@@ -283,10 +305,10 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
       }
     }
   };
-  auto i_of = [&](float ss) { return p.w_post ? rsqrtf(fmaf(ss, p.inv_d, p.eps)) : 1.f; };
-  auto token_gate = [&](int t) {
-    return p.gate_kind == MOE_GATE_TOKEN && t < p.T ? load1(p.gate, t, p.w_f32) : 1.f;
-  };
+  auto i_of = [&](float ss) { return post ? rsqrtf(fmaf(ss, p.inv_d, p.eps)) : 1.f; };
+  const bool tokens = p.gate_kind == MOE_GATE_TOKEN;
+  auto token_bits = [&](int t) { return tokens && t < p.T ? load1_bits(p.gate, t, p.w_f32) : 0u; };
+  auto gated = [&](float i_y, uint32_t bits) { return tokens ? i_y * value1(bits, p.w_f32) : i_y; };
 
   if (!kStaged) {                              // one row per row slot
     const int t = blockIdx.x * p.rows + row;
@@ -295,14 +317,14 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
       for (int j = 0; j < VPT; ++j)
         if (i0 + j * p.tpr < p.nvec) r[j] = load8(p.r, static_cast<size_t>(t) * p.nvec + i0 + j * p.tpr, RES32);
     }
-    const float g = token_gate(t);
+    const uint32_t g = token_bits(t);
     float sy[1] = {0.f};
-    if (p.w_post) {
+    if (post) {
       sy[0] = branch_square(t, nullptr);
       row_sums(sy, part[0], p.tpr);
     }
-    float sr[1] = {residual(t, nullptr, i_of(sy[0]) * g)};
-    if (!p.w_pre) return;
+    float sr[1] = {residual(t, nullptr, gated(i_of(sy[0]), g))};
+    if (!pre) return;
     row_sums(sr, part[1], p.tpr);
     normalised(t, sr[0]);
     return;
@@ -312,25 +334,27 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
   // number of turns.
   int t = blockIdx.x * p.rows + row;
   rows_wait<kStages>();                        // the first row (kStages - 1 are under way)
-  float sums[2] = {0.f, p.w_post ? branch_square(t, ring + threadIdx.x) : 0.f};
-  if (p.w_post) row_sums(sums, part[1], p.tpr);
+  float sums[2] = {0.f, post ? branch_square(t, ring + threadIdx.x) : 0.f};
+  if (post) row_sums(sums, part[1], p.tpr);
   int turn = 0;
+  uint32_t g = token_bits(t);
   for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, t += step, ++turn) {
-    const float g = token_gate(t);             // (under way while the rows are waited for)
+    const uint32_t g_next = token_bits(t + step);
     fetch(t + (kStages - 1) * step, (turn + kStages - 1) % kRing);
     rows_wait<kStages>();                      // row t + step
     const uint4* st = ring + turn % kRing * stage_vecs + threadIdx.x;
     const uint4* next = ring + (turn + 1) % kRing * stage_vecs + threadIdx.x;
-    sums[0] = residual(t, st, i_of(sums[1]) * g);
-    if (p.w_post) {
+    sums[0] = residual(t, st, gated(i_of(sums[1]), g));
+    g = g_next;
+    if (post) {
       sums[1] = branch_square(t + step, next);
       row_sums(sums, part[turn & 1], p.tpr);
-    } else if (p.w_pre) {
+    } else if (pre) {
       float one[1] = {sums[0]};
       row_sums(one, part[turn & 1], p.tpr);
       sums[0] = one[0];
     }
-    if (p.w_pre) normalised(t, sums[0]);
+    if (pre) normalised(t, sums[0]);
   }
 }
 
@@ -355,13 +379,17 @@ struct NormGradArgs {
 // (g_t the token or full gate, 1 with a channel gate, which is constant over tokens).  A thread
 // keeps those of its own vectors in registers (VPT <= 2) or in its own places of shared memory,
 // and writes them at the end as one partial per row slot.
-template <bool RES32, bool ACT32, int VPT, int kStages>
+//
+// Measured at T = 4095, d = 7168, bf16, both norms, channel gate, all gradients (352 MB): 70 us
+// with the sum of the partials, 5.0 TB/s, 0.77 of the measured copy bandwidth; bound by
+// instructions (about 45 per element) and the shared-memory reads of the three passes.
+template <bool RES32, bool ACT32, int VPT, int kStages, bool kAll = false>
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGradArgs p) {
   constexpr bool kSmem = VPT > 2, kStaged = kStages > 0;
   static_assert(!(kSmem && kStaged), "shared memory holds the column sums or the stages");
-  constexpr int kRing = kStaged ? kStages : 1;
+  constexpr int kRing = kStaged ? kStages : 1, kPitch = kStaged ? 512 : 0;
   constexpr int kR = RES32 ? 2 : 1, kY = ACT32 ? 2 : 1;
-  __shared__ float part[2][16 * 5];
+  __shared__ float part[2][32 * 5];
   extern __shared__ uint4 ring[];              // kSmem: fp32 column sums [2][d]
   float4* sums = reinterpret_cast<float4*>(ring);
   const int threads = blockDim.x;
@@ -384,8 +412,9 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
   };
   // stage: r' and dh (with the pre-norm), dr_out, y, full gate -- in fixed places
   constexpr int kAtDh = VPT * kR, kAtDr = kAtDh + VPT * kY, kAtY = kAtDr + VPT * kR, kAtGate = kAtY + VPT * kY;
-  const bool full_gate = p.gate_kind == MOE_GATE_FULL;
-  const int stage_vecs = (kAtGate + (full_gate ? VPT * kY : 0)) * threads;
+  const bool full_gate = !kAll && p.gate_kind == MOE_GATE_FULL;
+  const bool branch = kAll || p.y, post = kAll || p.w_post, pre = kAll || p.w_pre, upper = kAll || p.dr_out;
+  const int stage_vecs = (kAtGate + (full_gate ? VPT * kY : 0)) * kPitch;
   auto fetch = [&](int t, int s) {
     if (t < p.T) {
       uint4* st = ring + s * stage_vecs + threadIdx.x;
@@ -393,14 +422,14 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
         const int v = i0 + j * p.tpr;
-        if (v >= p.nvec) break;
-        if (p.w_pre) {
-          stage_in<RES32>(st, j, threads, p.rp, base + v);
-          stage_in<ACT32>(st + kAtDh * threads, j, threads, p.dh, base + v);
+        if (!kAll && v >= p.nvec) break;
+        if (pre) {
+          stage_in<RES32, kPitch>(st, j, p.rp, base + v);
+          stage_in<ACT32, kPitch>(st + kAtDh * kPitch, j, p.dh, base + v);
         }
-        if (p.dr_out) stage_in<RES32>(st + kAtDr * threads, j, threads, p.dr_out, base + v);
-        if (p.y) stage_in<ACT32>(st + kAtY * threads, j, threads, p.y, base + v);
-        if (full_gate) stage_in<ACT32>(st + kAtGate * threads, j, threads, p.gate, base + v);
+        if (upper) stage_in<RES32, kPitch>(st + kAtDr * kPitch, j, p.dr_out, base + v);
+        if (branch) stage_in<ACT32, kPitch>(st + kAtY * kPitch, j, p.y, base + v);
+        if (full_gate) stage_in<ACT32, kPitch>(st + kAtGate * kPitch, j, p.gate, base + v);
       }
     }
     rows_commit();
@@ -417,7 +446,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
   };
   auto branch_weight = [&](int v) {
     Vec8 a = constant8(1.f);
-    if (p.w_post) {
+    if (post) {
       a = load8(p.w_post, v, p.w_f32);
 #pragma unroll
       for (int e = 0; e < 4; ++e) a.p[e] = add2(a.p[e], both2(p.w_offset));
@@ -435,8 +464,8 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
       w[kSmem ? 0 : j] = c[kSmem ? 0 : j] = constant8(0.f);
-      if (v >= p.nvec) continue;
-      if (p.w_pre) w[kSmem ? 0 : j] = pre_weight(v);
+      if (!kAll && v >= p.nvec) continue;
+      if (pre) w[kSmem ? 0 : j] = pre_weight(v);
       c[kSmem ? 0 : j] = branch_weight(v);
     }
   }
@@ -449,10 +478,10 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (t >= p.T || v >= p.nvec) continue;
-      if (p.w_pre) {
-        const Vec8 x = row8<RES32, kStaged>(st, j, threads, p.rp, base + v);
-        const Vec8 z = row8<ACT32, kStaged>(st + kAtDh * threads, j, threads, p.dh, base + v);
+      if (t >= p.T || (!kAll && v >= p.nvec)) continue;
+      if (pre) {
+        const Vec8 x = row8<RES32, kPitch>(st, j, p.rp, base + v);
+        const Vec8 z = row8<ACT32, kPitch>(st + kAtDh * kPitch, j, p.dh, base + v);
         const Vec8 wj = kSmem ? pre_weight(v) : w[kSmem ? 0 : j];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -460,8 +489,8 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
           s1 = fma2(mul2(z.p[e], wj.p[e]), x.p[e], s1);
         }
       }
-      if (p.w_post) {
-        const Vec8 y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
+      if (post) {
+        const Vec8 y = row8<ACT32, kPitch>(st + kAtY * kPitch, j, p.y, base + v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s2 = fma2(y.p[e], y.p[e], s2);
       }
@@ -480,12 +509,12 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (v >= p.nvec) continue;
+      if (!kAll && v >= p.nvec) continue;
       Vec8 G = constant8(0.f);
-      if (p.dr_out) G = row8<RES32, kStaged>(st + kAtDr * threads, j, threads, p.dr_out, base + v);
-      if (p.w_pre) {
-        const Vec8 x = row8<RES32, kStaged>(st, j, threads, p.rp, base + v);
-        const Vec8 z = row8<ACT32, kStaged>(st + kAtDh * threads, j, threads, p.dh, base + v);
+      if (upper) G = row8<RES32, kPitch>(st + kAtDr * kPitch, j, p.dr_out, base + v);
+      if (pre) {
+        const Vec8 x = row8<RES32, kPitch>(st, j, p.rp, base + v);
+        const Vec8 z = row8<ACT32, kPitch>(st + kAtDh * kPitch, j, p.dh, base + v);
         const Vec8 wj = kSmem ? pre_weight(v) : w[kSmem ? 0 : j];
         Vec8 zx;
 #pragma unroll
@@ -498,8 +527,8 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
         if (kSmem && p.want_pre) smem_add(0, v, zx);
       }
       Vec8 y = constant8(0.f), g = constant8(1.f);
-      if (p.y) y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
-      if (full_gate) g = row8<ACT32, kStaged>(st + kAtGate * threads, j, threads, p.gate, base + v);
+      if (branch) y = row8<ACT32, kPitch>(st + kAtY * kPitch, j, p.y, base + v);
+      if (full_gate) g = row8<ACT32, kPitch>(st + kAtGate * kPitch, j, p.gate, base + v);
       if (p.res_scale != 1.f) {
         Vec8 o;
 #pragma unroll
@@ -508,7 +537,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
       } else {
         store8(p.dr, base + v, RES32, G);
       }
-      if (!p.y) continue;
+      if (!branch) continue;
       const Vec8 cj = kSmem ? branch_weight(v) : c[kSmem ? 0 : j];
       Vec8 b;
 #pragma unroll
@@ -538,16 +567,16 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
   };
   // 3: dy of row t
   auto branch_gradient = [&](int t, const uint4* st, float i_y, float qy, float gu) {
-    if (t >= p.T || !p.y) return;
+    if (t >= p.T || !branch) return;
     const size_t base = static_cast<size_t>(t) * p.nvec;
     const f32x2 k_y = both2(-i_y * i_y * i_y * (qy * p.inv_d));
     if (i0 == 0 && p.want_gate && p.gate_kind == MOE_GATE_TOKEN) static_cast<float*>(p.dgate)[t] = gu;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (v >= p.nvec) continue;
-      if (p.w_post) {
-        const Vec8 y = row8<ACT32, kStaged>(st + kAtY * threads, j, threads, p.y, base + v);
+      if (!kAll && v >= p.nvec) continue;
+      if (post) {
+        const Vec8 y = row8<ACT32, kPitch>(st + kAtY * kPitch, j, p.y, base + v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) q[j].p[e] = fma2(both2(i_y), q[j].p[e], mul2(k_y, y.p[e]));
       }
@@ -555,9 +584,12 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
     }
   };
   auto i_of = [&](float ss) { return rsqrtf(fmaf(ss, p.inv_d, p.eps)); };
-  auto scale_of = [&](int t) {                 // branch_scale (token gate)
-    return p.gate_kind == MOE_GATE_TOKEN && t < p.T ? p.branch_scale * load1(p.gate, t, p.w_f32) : p.branch_scale;
+  const bool tokens = p.gate_kind == MOE_GATE_TOKEN;
+  auto token_bits = [&](int t) { return tokens && t < p.T ? load1_bits(p.gate, t, p.w_f32) : 0u; };
+  auto scale_of = [&](uint32_t bits) {         // branch_scale (token gate)
+    return tokens ? p.branch_scale * value1(bits, p.w_f32) : p.branch_scale;
   };
+
   int t = blockIdx.x * p.rows + row;
   if (!kStaged) {
     // every thread of the CTA makes the same number of turns (row_sums synchronises it)
@@ -565,8 +597,8 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
       float s[3], m[2];
       squares(t, nullptr, s);
       row_sums(s, part[0], p.tpr);
-      const float i_y = p.w_post ? i_of(s[2]) : 1.f;
-      gradients(t, nullptr, scale_of(t), i_of(s[0]), s[1], i_y, m);
+      const float i_y = post ? i_of(s[2]) : 1.f;
+      gradients(t, nullptr, scale_of(token_bits(t)), i_of(s[0]), s[1], i_y, m);
       row_sums(m, part[1], p.tpr);
       branch_gradient(t, nullptr, i_y, m[0], m[1]);
     }
@@ -584,12 +616,12 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
     }
     int turn = 0;
     for (int t0 = blockIdx.x * p.rows; t0 < p.T; t0 += step, t += step, ++turn) {
-      const float tok = scale_of(t);
+      const uint32_t tok = token_bits(t);      // (under way while the rows are waited for)
       fetch(t + (kStages - 1) * step, (turn + kStages - 1) % kRing);
       rows_wait<kStages>();                    // row t + step
       const uint4* st = ring + turn % kRing * stage_vecs + threadIdx.x;
-      const float i_y = p.w_post ? i_of(s[2]) : 1.f;
-      gradients(t, st, tok, i_of(s[0]), s[1], i_y, s + 3);
+      const float i_y = post ? i_of(s[2]) : 1.f;
+      gradients(t, st, scale_of(tok), i_of(s[0]), s[1], i_y, s + 3);
       squares(t + step, ring + (turn + 1) % kRing * stage_vecs + threadIdx.x, s);
       row_sums(s, part[turn & 1], p.tpr);
       branch_gradient(t, st, i_y, s[3], s[4]);
@@ -603,7 +635,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = i0 + j * p.tpr;
-      if (v >= p.nvec) continue;
+      if (!kAll && v >= p.nvec) continue;
       Vec8 f;
       if (kSmem) f = load8(sums + a * (p.d / 4), v, true);
       else f = a == 0 ? A[kSmem ? 0 : j] : B[kSmem ? 0 : j];
@@ -684,25 +716,29 @@ constexpr size_t kSmemPerSm = 216 * 1024;
 
 template <bool RES32, bool ACT32, int VPT>
 cudaError_t launch_forward_typed(const NormArgs& a, cudaStream_t s) {
-  const int64_t turns = (static_cast<int64_t>(a.T) + a.rows - 1) / a.rows;
-  const int threads = a.tpr * a.rows;
   if constexpr (VPT > 1) {
-    // staged: three rows in flight per CTA, as many CTAs per SM as their stages leave room for
-    // (at most eight), if every CTA then gets at least three rows
-    constexpr int kStages = 3;
-    const size_t smem = static_cast<size_t>(kStages) * VPT * threads * 16 *
+    // staged: one CTA per SM with as many rows as its threads hold vectors for, kStages - 1 turns
+    // in flight, if every CTA gets at least that many.  (Two CTAs per SM leave 72 registers per
+    // thread, which spill: 94 us against 83 at T = 8192, d = 7168 without a gate.)
+    constexpr int kStages = VPT == 2 ? 4 : 3, kPitch = VPT == 2 ? 448 : 512;
+    const size_t smem = static_cast<size_t>(kStages) * VPT * kPitch * 16 *
                         ((RES32 ? 2 : 1) + ((a.y != nullptr) + (a.gate_kind == MOE_GATE_FULL)) * (ACT32 ? 2 : 1));
-    int ctas = static_cast<int>(kSmemPerSm / (smem + 1024));
-    if (ctas > 8) ctas = 8;
-    if (ctas >= 1 && turns >= 3 * kSms * ctas && threads <= (VPT == 2 ? 448 : 512)) {
-      const cudaError_t e = cudaFuncSetAttribute(block_norm_kernel<RES32, ACT32, VPT, kStages>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem));
+    NormArgs q = a;
+    q.rows = kPitch / a.tpr;                     // fill the CTA
+    const int threads = q.tpr * q.rows;
+    if (smem <= kSmemPerSm && q.rows >= 1 && a.T >= static_cast<int64_t>(kStages) * kSms * q.rows) {
+      const bool all = a.y && a.w_post && a.w_pre && a.r_out && a.gate_kind != MOE_GATE_FULL && a.nvec == VPT * a.tpr;
+      auto kernel = all ? block_norm_kernel<RES32, ACT32, VPT, kStages, true>
+                        : block_norm_kernel<RES32, ACT32, VPT, kStages, false>;
+      const cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return e;
-      block_norm_kernel<RES32, ACT32, VPT, kStages><<<kSms * ctas, threads, smem, s>>>(a);
+      kernel<<<kSms, threads, smem, s>>>(q);
       return cudaGetLastError();
     }
   }
+  const int64_t turns = (static_cast<int64_t>(a.T) + a.rows - 1) / a.rows;
+  const int threads = a.tpr * a.rows;
   block_norm_kernel<RES32, ACT32, VPT, 0><<<static_cast<unsigned>(turns), threads, 0, s>>>(a);
   return cudaGetLastError();
 }
@@ -719,14 +755,16 @@ cudaError_t launch_backward_typed(const NormGradArgs& a, unsigned grid, cudaStre
   const int threads = a.tpr * a.rows;
   if constexpr (VPT <= 2) {
     constexpr int kStages = 3;
-    const size_t smem = static_cast<size_t>(kStages) * VPT * threads * 16 *
+    const size_t smem = static_cast<size_t>(kStages) * VPT * 512 * 16 *
                         (2 * (RES32 ? 2 : 1) + (2 + (a.gate_kind == MOE_GATE_FULL)) * (ACT32 ? 2 : 1));
     if (smem <= kSmemPerSm && a.T > 2 * static_cast<int64_t>(grid) * a.rows) {
-      const cudaError_t e = cudaFuncSetAttribute(block_norm_backward_kernel<RES32, ACT32, VPT, kStages>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem));
+      const bool all = a.y && a.w_post && a.w_pre && a.dr_out && a.gate_kind != MOE_GATE_FULL && a.nvec == VPT * a.tpr;
+      auto kernel = all ? block_norm_backward_kernel<RES32, ACT32, VPT, kStages, true>
+                        : block_norm_backward_kernel<RES32, ACT32, VPT, kStages, false>;
+      const cudaError_t e =
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return e;
-      block_norm_backward_kernel<RES32, ACT32, VPT, kStages><<<grid, threads, smem, s>>>(a);
+      kernel<<<grid, threads, smem, s>>>(a);
       return cudaGetLastError();
     }
   }
