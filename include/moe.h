@@ -12,7 +12,9 @@
  *   h = silu(x W1^T) * (x W3^T);  y = h W2^T          moe_grouped_ffn per expert
  *   out[t] = sum_j w[t,j] y[row(t,j)] + shared(x[t])   moe_combine     [T, d]
  *
- * moe_layer_forward runs all of it on one stream.
+ * moe_layer_forward runs all of it on one stream.  Beside the layer: the norms around a
+ * block with its gate and residual scale (moe_block_norm), and the experts' products one at
+ * a time with their gradients (moe_grouped_gemm, bf16 or 8-bit with block scales).
  *
  * Conventions (all entry points):
  *  - Every pointer argument is caller-owned DEVICE memory unless stated.  The

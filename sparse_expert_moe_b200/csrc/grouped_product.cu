@@ -8,26 +8,21 @@
 //   y[r, j] = sum_b s_a[r, b] s_w[j / 128, b] (sum over block b of a[r, i] w[j, i]),
 // the inner sums on the tensor cores, the outer one in fp32 registers.
 //
-// Two kernels share a scheduler.  Both put the weight index on the MMA's M side (128 lanes of
-// TMEM per CTA) and the group's tokens on its N side, so a group of few rows costs a narrow
-// MMA; TN has the weight's n index on M and its k index on N.
+// Three kernels.  Each tile is one accumulator in TMEM, whose M side is its 128 lanes per CTA.
 //
-//   stream_kernel  groups of few rows: HBM-bound on the weights.  One CTA per SM, tiles of
-//                  256 weight rows x 32 tokens.  All tiles' K blocks form one sequence, cut
-//                  into equal contiguous pieces, one per CTA, so every SM streams the same
-//                  number of weight bytes whatever the groups are.
-//   pair_kernel    larger groups, and every TN product: two CTAs share 256 x 256 tiles
-//                  (cta_group::2), each staging 128 rows of either operand, which halves the
-//                  shared-memory fill per flop of 128-row tiles.  Whole rounds of tiles go
-//                  to the pairs in an order that keeps a few weight blocks and token tiles in
-//                  L2; the K blocks of the last, partial round are cut equally as above.
+//   stream_kernel  NT (either type), NN on groups of few rows
+//   pair_kernel    NT, NN in bf16 on larger groups; every TN
+//   fold_kernel    NT in e4m3 on larger groups
 //
 // A tile whose K blocks fell to several CTAs is joined without waiting: each writes its fp32
 // sums to the workspace, and the one that arrives last (a counter in the workspace header)
 // adds all of them in K order, so that results do not depend on who was last.
 //
-// Warp roles: 0 TMA producer, 1 MMA issuer (and TMEM owner), 2 scales (e4m3) or the zeroing of
-// rows behind a group's last (TN), 3.. epilogue.
+// Warp roles: 0 TMA producer, 1 MMA issuer (and TMEM owner), 2 scales (stream kernel, e4m3) or
+// the zeroing of rows behind a group's last (TN), then the epilogue warps.  Producer and issuer
+// keep the whole warp in their loops and let one elected lane issue: TMA and MMA instructions take
+// their operands from uniform registers, and a branch on the lane number costs a transfer for
+// each of them (pair kernel, TN, 8192 x 4096 x 7168: 1274 TFLOP/s so, 1460 uniform).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
@@ -46,7 +41,7 @@ constexpr uint32_t kBox = 64 * 128;             // one 64-row box of 128-byte ro
 constexpr uint32_t kTileA = 2 * kBox;           // 128 x 128 bytes
 constexpr int kCounterWord0 = 16;               // header words 16..63: four 8-bit counters each
 constexpr int kMaxCounters = 192;
-constexpr int kScaleBlocks = 8;                 // K blocks of scales fetched at a time
+constexpr int kScaleBlocks = 8;                 // stream kernel: K blocks of scales fetched at a time
 
 struct ProductArgs {
   CUtensorMap wmap;             // NT, NN: weights [G][n][k]; TN: dy [rows][n]
@@ -413,6 +408,16 @@ __device__ __forceinline__ void join_parts(float* v, Slot slot, int first, int l
 }
 
 // ------------------------------------------------------------------ stream kernel
+// Groups of few rows: every weight byte is used for a handful of tokens, so HBM bounds it and the
+// tile is made for a steady stream.  The weights are the M side (256 rows per tile, two MMAs), the
+// tokens the N side (16 or 32), so that a token costs a narrow MMA and not a padded one.  All
+// tiles' K blocks form one sequence that is cut evenly over the SMs, whatever the groups are: every
+// SM streams the same number of bytes, five stages of 32 KB of weights ahead.
+//
+// Measured: 64 groups, n = 7168, k = 2048, 512 rows: 6.43 TB/s (0.98 of a copy); one token's 8
+// groups of n = 4096, k = 7168 80 us (5.9 TB/s: about 8 us are launch, first loads and the
+// join of the cut tiles).  One e4m3 token, n = 7168, k = 2048: 10.3 us, latency: the start of
+// the CTA and its first loads, three K blocks, the join of the parts.
 template <bool F8, int OP>
 struct StreamCfg {
   static constexpr int kMB = 2;                                   // 128-row weight blocks per tile
@@ -700,6 +705,19 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ pair kernel
+// bf16 on larger groups, and every TN product: two CTAs share 256 x 256 tiles (cta_group::2), each
+// staging 128 rows of either operand, which halves the shared-memory fill per flop of
+// 128-row tiles.  The weight index is the M side and the group's tokens are the N side in steps of
+// 32, so a short group costs a narrow MMA; TN has the weight's n index on M, its k index on N.
+// Whole rounds of tiles go to the pairs in an order that keeps a few weight blocks and token
+// tiles in L2; the K blocks of a partial last round are cut.  Two accumulators take turns, so the
+// epilogue of a tile runs under the next tile's MMAs.
+//
+// Measured: one group of 8192 rows, n = 4096, k = 7168: 320 us for NT and TN (1500 TFLOP/s), 370
+// for NN; one K block takes 513 cycles, of which the MMAs need 512, and the 1000 W power limit
+// holds the clock near 1.2 GHz in a loop of them.  TN of 32 groups x 256 rows, n = 7168, k = 2048,
+// fp32: 388 us, 4.8 TB/s of stores; a tile has four K blocks there for 256 KB of sums, so the
+// stores bound it.  Eight epilogue warps measured 394 us.
 constexpr size_t kPartFloats = 128 * 256;       // a CTA's sums of a cut tile
 
 template <int OP>
@@ -713,7 +731,6 @@ struct PairCfg {
   static constexpr int kThreads = 32 * (kEpi0 + kEpi);
   static constexpr uint32_t kWarpStage = OP == kTN ? 2 * 4096 : 2048;
   static constexpr uint32_t kStaging = kEpi * kWarpStage;
-           // both CTAs
   static constexpr uint32_t kSmem =
       1024 + kStages * kStage + 1024 + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
   static_assert(kSmem <= 227 * 1024, "budget");
