@@ -234,19 +234,21 @@ struct EvenShare {
   }
 };
 
-// Pair kernel: whole tiles me, me + n, ...; the tiles of a last round that would leave at least
-// half of the pairs idle are cut into `parts` equal runs of K blocks, one per pair.  Joining a
-// 256 x 256 tile costs about eight K blocks' time per part, so a part has 24 at least, and
-// there are at most four.
+// Pair and fold kernels: whole tiles me, me + n, ...; the tiles of a last round that would leave
+// at least half of the pairs (CTAs) idle are cut into `parts` equal runs of K blocks, one per pair.
+// A join costs about what min_kb K blocks do, so a part has that many at least, and there are at
+// most four.  Measured: 24 in the pair kernel; 14 in the fold kernel, whose K blocks are twice as
+// long (128 rows, n = 4096, k = 7168: 29.0 us in two parts, 25.0 in four; k = 2048 in two parts 20.3
+// us against 18.0 whole).
 struct RoundShare {
   int me, n, kb, whole, parts, cut_tiles, at;
   bool part_left;               // this pair's part of a cut tile is still to come
 
-  __device__ __forceinline__ RoundShare(int me_, int n_, int n_tiles, int kb_, bool may_cut)
+  __device__ __forceinline__ RoundShare(int me_, int n_, int n_tiles, int kb_, bool may_cut, int min_kb)
       : me(me_), n(n_), kb(kb_), whole(n_tiles), parts(1), cut_tiles(0), at(me_) {
     const int rest = n_tiles % n;
     if (may_cut && rest > 0) {
-      parts = min(min(n / rest, kb / 24), 4);
+      parts = min(min(n / rest, kb / min_kb), 4);
       if (parts > 1) {
         cut_tiles = rest;
         whole = n_tiles - rest;
@@ -795,7 +797,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   // K blocks of a tile (TN: of the only group; with several, tiles differ and are not cut)
   const int kb_all = OP == kTN ? (n_tiles ? (gt.off[1] - gt.off[0] + 63) / 64 : 1) : p.k_blocks;
-  RoundShare sched(pair, n_pairs, n_tiles, kb_all, OP != kTN || p.n_groups == 1);
+  RoundShare sched(pair, n_pairs, n_tiles, kb_all, OP != kTN || p.n_groups == 1, 24);
   // The next piece of work and its tile; a whole TN tile has its own group's K blocks.
   Piece c;
   Tile t;
@@ -1086,12 +1088,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
 // is folded by eight warps -- 128 fp32 sums per thread, packed two to an instruction, each
 // 16-column load under way during the previous one's arithmetic -- the MMAs fill the other.
 //
-// Measured at that size: 252 us, 1906 TFLOP/s, 0.72 of cuBLASLt's plain e4m3 rate (sustained).
-// What bounds it is the turn of a buffer: about 1200 cycles per K block, of which the MMAs need
-// 512 at full rate and about 750 with their operands read from one CTA's shared memory.  On the
-// way there: two 128-column MMAs and four buffers 312 us (the token operand is read twice),
-// sixteen epilogue warps 365 us (twice the waits), K blocks not unrolled 295 us, scales fetched
-// four K blocks ahead instead of two 260 us (registers spill).
+// One commit per K block says both that its products are in TMEM and that its stage is free.  The
+// scales come through shared memory, fetched by the two warps that are free otherwise.
+//
+// Measured at that size: 243 us, 1980 TFLOP/s, 0.75 of cuBLASLt's plain e4m3 rate (sustained).
+// A K block takes about 1040 cycles, of which the MMAs need 512 at full rate.  Loads alone, with
+// neither MMAs nor folds, take 146 us there, loads and MMAs 200 us, loads and folds 200 us: what
+// is left is that the two overlap in part only, with the two buffers that TMEM has room for.  On
+// the way: two 128-column MMAs and four buffers 312 us (the token operand is read twice), sixteen
+// epilogue warps 365 us (twice the waits), scales loaded by the epilogue threads two K blocks ahead
+// 254 us, 32-column loads two at a time 318 us (registers spill).  CTA pairs with 256 tokens:
+// 245 us, and 450 us where 64 groups have 16 rows each (293 us here); pairs on 128-column tiles
+// with four buffers 307 us.
 struct FoldCfg {
   static constexpr int kWidth = 128;                              // tokens
   static constexpr uint32_t kStage = 3 * kTileA;                  // 128 token + 256 weight rows: 48 KB
@@ -1099,12 +1107,14 @@ struct FoldCfg {
   static constexpr int kCols = 256;                               // per buffer
   static constexpr int kThreads = 384;
   // an epilogue thread keeps 128 sums and 32 products: registers move from warps 0..3 to 4..11.
-  // 384 x 168 at launch = 128 x 56 + 256 x 224.
-  static constexpr int kRegsLow = 56, kRegsHigh = 224;
-  static constexpr uint32_t kWarpStage = 2048;
+  // 384 x 168 at launch = 128 x 40 + 256 x 232.
+  static constexpr int kRegsLow = 40, kRegsHigh = 232;
+  static constexpr uint32_t kWarpStage = 1024;
   static constexpr uint32_t kStaging = 8 * kWarpStage;
+  static constexpr int kRowScales = 128 + 2;                      // per K block: tokens, weight blocks
+  static constexpr uint32_t kScales = 2 * kScaleBlocks * kRowScales * 4;
   static constexpr uint32_t kSmem =
-      1024 + kStages * kStage + 1024 + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
+      1024 + kStages * kStage + 1024 + kScales + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
   static_assert(kSmem <= 227 * 1024, "budget");
 };
 
@@ -1115,14 +1125,16 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(tiles + C::kStages * C::kStage);
-  uint64_t* empty_bar = full_bar + C::kStages;
-  uint64_t* tfull_bar = empty_bar + C::kStages;       // [2]
-  uint64_t* tempty_bar = tfull_bar + 2;
-  uint64_t* epi_bar = tempty_bar + 2;
+  uint64_t* done_bar = full_bar + C::kStages;         // a stage's products are in TMEM, the stage is free
+  uint64_t* tempty_bar = done_bar + C::kStages;       // [2] buffers read
+  uint64_t* sfull_bar = tempty_bar + 2;               // [2] scales of kScaleBlocks K blocks
+  uint64_t* sempty_bar = sfull_bar + 2;
+  uint64_t* epi_bar = sempty_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* last_flag = reinterpret_cast<int*>(tmem_slot + 2);
-  uint8_t* staging = tiles + C::kStages * C::kStage + 1024;
+  float* scales = reinterpret_cast<float*>(tiles + C::kStages * C::kStage + 1024);
+  uint8_t* staging = reinterpret_cast<uint8_t*>(scales) + C::kScales;
   GroupTable& gt = *reinterpret_cast<GroupTable*>(staging + C::kStaging);
   int* status = p.header;
 
@@ -1130,11 +1142,12 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full_bar[i], 1);
-      mbar_init(&empty_bar[i], 1);
+      mbar_init(&done_bar[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&tfull_bar[i], 1);
       mbar_init(&tempty_bar[i], 8);
+      mbar_init(&sfull_bar[i], 64);                    // threads of the scale warps
+      mbar_init(&sempty_bar[i], 8);
     }
     mbar_init(epi_bar, 8);
     *abort_flag = 0;
@@ -1152,7 +1165,7 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  RoundShare sched(blockIdx.x, gridDim.x, n_tiles, p.k_blocks, true);
+  RoundShare sched(blockIdx.x, gridDim.x, n_tiles, p.k_blocks, true, 14);
   Piece c;
   Tile t;                                        // mb: block of 256 weight rows
   auto fetch = [&]() {
@@ -1173,7 +1186,7 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
       while (ok && fetch()) {
         const int n_pad = (t.rows + 15) & ~15, nh = halves();
         for (int kb = c.kb0; kb < c.kb1; ++kb) {
-          ok = mbar_poll_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
+          ok = mbar_poll_warp(&done_bar[stage], phase ^ 1u, abort_flag, status);
           if (!ok) break;
           uint8_t* st = tiles + stage * C::kStage;
           uint64_t* bar = &full_bar[stage];
@@ -1218,8 +1231,7 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
             for (int kk = 0; kk < 4; ++kk)
               umma_e4m3(tmem + b * C::kCols, umma_desc_sw128(sa + kk * 32), umma_desc_sw128(sb + kk * 32), idesc,
                         kk ? 1u : 0u);
-            umma_commit(&tfull_bar[b]);
-            umma_commit(&empty_bar[stage]);
+            umma_commit(&done_bar[stage]);
           }
           __syncwarp();
           if (++stage == C::kStages) {
@@ -1228,16 +1240,43 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
           }
         }
       }
+    } else {
+      // -------------------------------------------------------- scales
+      // Warps 2 and 3 copy the scales of kScaleBlocks K blocks at a time to [K block][token], with
+      // the two weight blocks' behind the tokens'; rows past the tile repeat its last.
+      const int me = (warp - 2) * 32 + lane;
+      uint32_t it = 0;
+      bool ok = true;
+      while (ok && fetch()) {
+        const float* sa0 = p.a_scale + static_cast<size_t>(t.row0 + min(me, t.rows - 1)) * p.k_blocks;
+        const float* sa1 = p.a_scale + static_cast<size_t>(t.row0 + min(me + 64, t.rows - 1)) * p.k_blocks;
+        const float* sw = p.w_scale + (static_cast<size_t>(t.g) * p.w_scale_rows +
+                                       min(2 * t.mb + (lane & 1), p.w_scale_rows - 1)) * p.k_blocks;
+        for (int kb = c.kb0; kb < c.kb1; kb += kScaleBlocks, ++it) {
+          ok = mbar_poll_warp(&sempty_bar[it & 1], ((it >> 1) & 1u) ^ 1u, abort_flag, status);
+          if (!ok) break;
+          float* dst = scales + (it & 1) * (kScaleBlocks * C::kRowScales);
+          const int last = c.kb1 - 1;
+#pragma unroll
+          for (int q = 0; q < kScaleBlocks; ++q) {
+            cp_async_4(dst + q * C::kRowScales + me, sa0 + min(kb + q, last));
+            cp_async_4(dst + q * C::kRowScales + me + 64, sa1 + min(kb + q, last));
+          }
+          if (warp == 2 && lane < 2 * kScaleBlocks)
+            cp_async_4(dst + (lane >> 1) * C::kRowScales + 128 + (lane & 1), sw + min(kb + (lane >> 1), last));
+          cp_async_mbar_arrive_noinc(&sfull_bar[it & 1]);
+        }
+      }
+      cp_async_wait_all();
     }
   } else {
     // ---------------------------------------------------------- epilogue
     regs_up<C::kRegsHigh>();
-    constexpr int kRun = 2;                      // K blocks of scales fetched at a time
     const int sub = warp & 3;                    // TMEM lane quadrant: tokens sub * 32 + lane
     const int half = (warp - 4) >> 2;            // 128-column half of the tile
     uint8_t* stg = staging + (warp - 4) * C::kWarpStage;
     EpilogueSync sync{epi_bar, abort_flag, status};
-    uint32_t it = 0;
+    uint32_t it = 0, sit = 0;
     bool ok = true;
     while (ok && fetch()) {
       const int col0 = t.mb * 256 + half * 128;  // the warp's first output column
@@ -1246,35 +1285,22 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
       f32x2 acc[64];                             // 128 sums
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = both2(0.f);
-      const float* sa = p.a_scale + static_cast<size_t>(t.row0 + min(sub * 32 + lane, t.rows - 1)) * p.k_blocks;
-      const float* sw = p.w_scale + (static_cast<size_t>(t.g) * p.w_scale_rows +
-                                     min(2 * t.mb + half, p.w_scale_rows - 1)) * p.k_blocks;
-      float next_a[kRun], next_w[kRun], f[kRun];
-      auto scales = [&](int kb) {
-#pragma unroll
-        for (int q = 0; q < kRun; ++q) {
-          next_a[q] = __ldg(sa + min(kb + q, c.kb1 - 1));
-          next_w[q] = __ldg(sw + min(kb + q, c.kb1 - 1));
-        }
-      };
-      if (mine) scales(c.kb0);
-      for (int kb0 = c.kb0; kb0 < c.kb1 && ok; kb0 += kRun) {
-        if (mine) {
-#pragma unroll
-          for (int q = 0; q < kRun; ++q) f[q] = next_a[q] * next_w[q];
-          if (kb0 + kRun < c.kb1) scales(kb0 + kRun);
-        }
-#pragma unroll
-        for (int r = 0; r < kRun; ++r) {
+      for (int kb0 = c.kb0; kb0 < c.kb1 && ok; kb0 += kScaleBlocks, ++sit) {
+        ok = mbar_poll_warp(&sfull_bar[sit & 1], (sit >> 1) & 1u, abort_flag, status);
+        if (!ok) break;
+        const float* sc = scales + (sit & 1) * (kScaleBlocks * C::kRowScales);
+#pragma unroll 2
+        for (int r = 0; r < kScaleBlocks; ++r) {
           if (kb0 + r >= c.kb1) break;
           const uint32_t b = it & 1u;
-          ok = mbar_poll_warp(&tfull_bar[b], (it >> 1) & 1u, abort_flag, status);
+          const float f = sc[r * C::kRowScales + sub * 32 + lane] * sc[r * C::kRowScales + 128 + half];
+          ok = mbar_poll_warp(&done_bar[it % C::kStages], (it / C::kStages) & 1u, abort_flag, status);
           if (!ok) break;
           ++it;
           tc_fence_after();
           if (mine) {
             const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols + half * 128;
-            const f32x2 gg = both2(f[r]);
+            const f32x2 gg = both2(f);
             uint32_t v[2][16];
             tmem_ld16_begin(tb, v[0]);
             tmem_ld_end(v[0]);
@@ -1297,6 +1323,8 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
             mbar_arrive(&tempty_bar[b]);
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty_bar[sit & 1]);
       }
       if (!ok) break;
       auto finish = [&](const float* v, int i) {

@@ -394,6 +394,8 @@ __device__ __forceinline__ void cp_async_mbar_arrive_noinc(uint64_t* bar) {
                : "memory");
 }
 
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // Orders this thread's view of shared memory between the generic proxy (plain and
 // cp.async writes) and the async proxy (TMA, tcgen05 reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {
