@@ -279,7 +279,8 @@ def _device_of(*tensors) -> int:
     """Index of the CUDA device of the first tensor among them (-1: only addresses)."""
     for t in tensors:
         if t is not None and type(t) is not int:
-            return t.get_device() if t.is_cuda else -2
+            d = t.get_device()
+            return d if d >= 0 else -2
     return -1
 
 
@@ -313,7 +314,7 @@ def _call(fn: str, device: int, stream, *args):
     f = getattr(_lib or load_library(), fn)
     if device < 0:
         code = f(*args, _stream(stream))
-    elif device == torch.cuda.current_device():
+    elif device == torch._C._cuda_getDevice():       # its tensors have initialised CUDA
         code = f(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(device):
