@@ -1,0 +1,194 @@
+"""Calls of the block norms and the grouped products that their documentation allows and that the
+tests of their formulas do not make: outputs in place of inputs at sizes where rows are staged
+ahead, tensors aligned to their elements or to 16 bytes only, the largest number of groups, a row
+of NaN beside others."""
+import numpy as np
+import pytest
+import torch
+
+from sparse_expert_moe_b200 import moe
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = torch.bfloat16
+
+
+def randn(seed, *shape, dtype=BF):
+    g = torch.Generator(DEV).manual_seed(seed)
+    return torch.randn(*shape, device=DEV, generator=g).to(dtype)
+
+
+def shifted(t, elements):
+    """The same values in memory that starts `elements` behind an allocation's start."""
+    flat = torch.empty(t.numel() + elements, device=t.device, dtype=t.dtype)
+    out = flat[elements:].view(t.shape)
+    out.copy_(t)
+    return out
+
+
+def same(a, b):
+    """Equal, NaN with NaN (an e4m3 conversion of values past 448 leaves NaN codes)."""
+    return torch.allclose(a, b, rtol=0, atol=0, equal_nan=True)
+
+
+def norm_ws(cfg):
+    return torch.empty(moe.moe_norm_workspace_size(cfg), dtype=torch.uint8, device=DEV)
+
+
+def product_ws(cfg):
+    return torch.zeros(moe.moe_product_workspace_size(cfg), dtype=torch.uint8, device=DEV)
+
+
+# ------------------------------------------------------------------------------------ norms
+@pytest.mark.parametrize("T,d", [(3, 7168), (1501, 7168), (4001, 1024), (700, 16384), (5003, 264)])
+@pytest.mark.parametrize("gate", ["channel", "full"])
+def test_forward_in_place(T, d, gate):
+    r, y, w = randn(1, T, d), randn(2, T, d), randn(3, d)
+    g = randn(4, d) if gate == "channel" else randn(4, T, d)
+    cfg = moe.make_norm_config(T, d, gate=gate)
+    want_r, want_h = torch.empty_like(r), torch.empty_like(r)
+    moe.moe_block_norm(cfg, r, y, w, g, w, want_r, want_h, None)
+    for place in ("y", "r"):
+        a, b = r.clone(), y.clone()
+        if place == "y":                         # r' over r, h over y
+            moe.moe_block_norm(cfg, a, b, w, g, w, a, b, None)
+            assert torch.equal(a, want_r) and torch.equal(b, want_h)
+        else:                                    # h over r, r' not kept
+            moe.moe_block_norm(cfg, a, b, w, g, w, None, a, None)
+            assert torch.equal(a, want_h) and torch.equal(b, y)
+
+
+@pytest.mark.parametrize("T,d", [(3, 7168), (1501, 7168), (4001, 1024), (300, 16384), (5003, 264)])
+@pytest.mark.parametrize("gate", ["token", "full"])
+def test_backward_in_place(T, d, gate):
+    r, y, dh, dr, w = randn(1, T, d), randn(2, T, d), randn(5, T, d), randn(6, T, d), randn(3, d)
+    g = randn(4, T) if gate == "token" else randn(4, T, d)
+    cfg = moe.make_norm_config(T, d, gate=gate)
+    ws = norm_ws(cfg)
+
+    def call(y, dh, dr_out, dr_in, dy):
+        dg = torch.empty_like(g, dtype=torch.float32 if gate == "token" else BF)
+        dp, dq = torch.empty(d, device=DEV), torch.empty(d, device=DEV)
+        moe.moe_block_norm_backward(cfg, r, y, w, g, w, dh, dr_out, dr_in, dy, dg, dp, dq, ws)
+        return dr_in, dy, dg, dp, dq
+    want = call(y, dh, dr, torch.empty_like(r), torch.empty_like(y))
+    a, b, c = y.clone(), dh.clone(), dr.clone()
+    for got in (call(y, b, c, c, b), call(a, dh, dr, torch.empty_like(r), a)):
+        for x, z in zip(got, want):
+            assert torch.equal(x, z)
+
+
+@pytest.mark.parametrize("T", [5, 2003])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_token_gates_and_scales_aligned_to_their_elements(T, dtype):
+    d = 1024
+    r, y, w, g = randn(1, T, d), randn(2, T, d), randn(3, d, dtype=dtype), randn(4, T, dtype=dtype)
+    cfg = moe.make_norm_config(T, d, gate="token", weight="bf16" if dtype == BF else "f32", out="e4m3")
+    got = []
+    for gate, scale in ((g, torch.empty(T, d // 128, device=DEV)),
+                        (shifted(g, 1), torch.empty(T * d // 128 + 1, device=DEV)[1:].view(T, d // 128))):
+        h = torch.empty(T, d, device=DEV, dtype=torch.float8_e4m3fn)
+        rp = torch.empty_like(r)
+        moe.moe_block_norm(cfg, r, y, w, gate, w, rp, h, scale)
+        dy, dr, dg = torch.empty_like(y), torch.empty_like(r), torch.empty(T + 1, device=DEV)[1:]
+        moe.moe_block_norm_backward(cfg, rp, y, w, gate, w, y, r, dr, dy, dg, None, None, norm_ws(cfg))
+        got.append((h.view(torch.uint8), scale, rp, dy, dr, dg))
+    for x, z in zip(*got):
+        assert torch.equal(x, z)
+
+
+@pytest.mark.parametrize("T,d", [(7, 264), (2003, 7168)])
+def test_norm_tensors_aligned_to_16_bytes(T, d):
+    r, y, w, g = randn(1, T, d), randn(2, T, d), randn(3, d), randn(4, d)
+    cfg = moe.make_norm_config(T, d, gate="channel")
+    want = [torch.empty_like(r), torch.empty_like(r)]
+    moe.moe_block_norm(cfg, r, y, w, g, w, *want, None)
+    got = [shifted(torch.zeros_like(r), 8), shifted(torch.zeros_like(r), 24)]
+    moe.moe_block_norm(cfg, shifted(r, 8), shifted(y, 40), shifted(w, 8), shifted(g, 16), shifted(w, 56), *got, None)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------------------------ products
+def product(op, sizes, n, k, move=0, mark=None, out="bf16"):
+    """One call; `move`: elements that every operand is moved by, `mark`: a row of NaN."""
+    R, G = sum(sizes), len(sizes)
+    fp8 = op == "fp8"
+    cfg = moe.make_product_config(G, R, n, k, dtype="e4m3_fs" if fp8 else "bf16", out=out)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device=DEV)
+    x, w = randn(1, R, n if op == "dgrad" else k), randn(2, G, n, k)
+    dy = randn(5, R, n)
+    sa = sw = None
+    if fp8:
+        x, w = (100 * x.float()).to(torch.float8_e4m3fn), (100 * w.float()).to(torch.float8_e4m3fn)
+        sa = shifted(randn(6, R, -(-k // 128)).float(), move // 16)
+        sw = shifted(randn(7, G, -(-n // 128), -(-k // 128)).float(), move // 16)
+    if mark is not None:
+        if fp8:
+            x.view(torch.uint8)[mark] = 0x7F
+        else:
+            x[mark] = float("nan")
+    x, w, dy = shifted(x, move), shifted(w, move), shifted(dy, move)
+    shape = {"gemm": (R, n), "fp8": (R, n), "dgrad": (R, k), "wgrad": (G, n, k)}[op]
+    y = shifted(torch.full(shape, -7.0, device=DEV, dtype=BF if out == "bf16" else torch.float32), move)
+    ws = product_ws(cfg)
+    if op == "dgrad":
+        moe.moe_grouped_gemm_dgrad(cfg, off, x, w, y, ws)
+    elif op == "wgrad":
+        moe.moe_grouped_gemm_wgrad(cfg, off, dy, x, y, ws)
+    else:
+        moe.moe_grouped_gemm(cfg, off, x, sa, w, sw, y, ws)
+    assert moe.moe_read_device_status(ws) == 0 and (ws[:256] == 0).all()
+    return y
+
+
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "wgrad", "fp8"])
+@pytest.mark.parametrize("sizes", [[1, 0, 6], [150, 3, 290]])
+def test_operands_aligned_to_16_bytes(op, sizes):
+    for out in ("bf16", "f32"):
+        assert same(product(op, sizes, 264, 400, out=out), product(op, sizes, 264, 400, move=16, out=out))
+
+
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "fp8"])
+@pytest.mark.parametrize("sizes,mark", [([3], 1), ([20, 0, 30], 25), ([300, 5], 140), ([90, 260], 91)])
+def test_a_row_of_nan_stays_alone(op, sizes, mark):
+    clean, got = product(op, sizes, 264, 400), product(op, sizes, 264, 400, mark=mark)
+    assert torch.isnan(got[mark]).all()
+    keep = [i for i in range(sum(sizes)) if i != mark]
+    assert same(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("op", ["gemm", "dgrad", "wgrad", "fp8"])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_most_groups(op, rows):
+    """1024 groups, most of them empty, against sums in 64 bits."""
+    sizes = [0] * 1024
+    for g in (0, 5, 511, 512, 1023):
+        sizes[g] = rows
+    n, k = 136, 64
+    got = product(op, sizes, n, k, out="f32")
+    R = sum(sizes)
+    x, w = randn(1, R, n if op == "dgrad" else k), randn(2, 1024, n, k)
+    lo = 0
+    for g, m in enumerate(sizes):
+        if op == "wgrad":
+            if m == 0:
+                assert (got[g] == 0).all()
+                continue
+            ref, mag = [f(randn(5, R, n)[lo:lo + m].double()).T @ f(x[lo:lo + m].double()) for f in (lambda v: v, abs)]
+            inner, have = m, got[g]
+        elif m == 0:
+            continue
+        elif op == "fp8":
+            q, v = (100 * x.float()).to(torch.float8_e4m3fn), (100 * w[g].float()).to(torch.float8_e4m3fn)
+            s = randn(6, R, 1).float().double()[lo:lo + m] * randn(7, 1024, 2, 1).float().double()[g].repeat_interleave(128, 0)[:n].T
+            ref = (q[lo:lo + m].double() @ v.double().T) * s
+            mag = (q[lo:lo + m].double().abs() @ v.double().T.abs()) * s.abs()
+            inner, have = k, got[lo:lo + m]
+        else:
+            wm = w[g].double().T if op == "gemm" else w[g].double()
+            ref, mag = x[lo:lo + m].double() @ wm, x[lo:lo + m].double().abs() @ wm.abs()
+            inner, have = x.shape[1], got[lo:lo + m]
+        lo += m
+        # each of the inner + inner / 16 addends cut at 2^-23 of the largest; two scales: 3 roundings
+        tol = ((inner + inner / 16 + 16) * 2.0 ** -23 + 3 * 2.0 ** -24) * mag + 2.0 ** -24 * ref.abs()
+        assert (((have.double() - ref).abs() <= tol) | (torch.isnan(have) & torch.isnan(ref))).all(), g
