@@ -159,11 +159,12 @@ __device__ __forceinline__ Vec8 row8(const uint4* st, int slot, const void* base
 // into registers: c = branch_scale (w_post + o) (channel gate), and w_pre + o.
 //
 // Bound by HBM where rows are many.  Measured at T = 8192, d = 7168, bf16, post-norm, token gate
-// and pre-norm (470 MB): 74 us, 6.3 TB/s, 0.97 of the measured copy bandwidth.  On the way there:
+// and pre-norm (470 MB): 73 us, 6.4 TB/s, 0.98 of the measured copy bandwidth.  On the way there:
 // one row per CTA, weights fetched per row 172 us (a row's loads and its two sums took turns);
 // rows staged 134 us (50 instructions per element, issued 57% of the time); packed arithmetic, the
 // weights in registers, one barrier per row 96 us; no tests per vector, one CTA per SM without
-// spills and the token gate's bits fetched a row ahead 74 us.
+// spills and the token gate's bits fetched a row ahead 74 us; launches that overlap 73 us (the
+// backward 70 -> 67 us, one token 4.0 -> 3.8 us).
 //
 // kAll (staged): a branch with its norm, no full gate, both outputs and no vectors past the row's
 // end -- what a block normally has -- without the tests for it per vector.
@@ -195,6 +196,8 @@ __global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 
     }
     rows_commit();
   };
+  launch_wait();
+  launch_begin_next();
   if (kStaged)
     for (int s = 0; s + 1 < kStages; ++s) fetch(blockIdx.x * p.rows + row + s * step, s);
 
@@ -380,7 +383,7 @@ struct NormGradArgs {
 // keeps those of its own vectors in registers (VPT <= 2) or in its own places of shared memory,
 // and writes them at the end as one partial per row slot.
 //
-// Measured at T = 4095, d = 7168, bf16, both norms, channel gate, all gradients (352 MB): 70 us
+// Measured at T = 4095, d = 7168, bf16, both norms, channel gate, all gradients (352 MB): 67 us
 // with the sum of the partials, 5.0 TB/s, 0.77 of the measured copy bandwidth; bound by
 // instructions (about 45 per element) and the shared-memory reads of the three passes.
 template <bool RES32, bool ACT32, int VPT, int kStages, bool kAll = false>
@@ -395,6 +398,8 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
   const int threads = blockDim.x;
   const int row = threadIdx.x / p.tpr, i0 = threadIdx.x - row * p.tpr;
   const int step = gridDim.x * p.rows;
+  launch_wait();
+  launch_begin_next();
   Vec8 A[kSmem ? 1 : VPT], B[kSmem ? 1 : VPT];
   if (kSmem) {
     for (int i = threadIdx.x; i < p.d / 2; i += threads) sums[i] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -649,6 +654,8 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
 __global__ void __launch_bounds__(256) sum_parts_kernel(const NormGradArgs p, float* dw_pre, float* dw_post,
                                                         float* dgate) {
   __shared__ float s[8][33];
+  launch_wait();
+  launch_begin_next();
   const bool branch = blockIdx.y != 0;
   if (branch ? !p.want_branch : !p.want_pre) return;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -733,14 +740,12 @@ cudaError_t launch_forward_typed(const NormArgs& a, cudaStream_t s) {
       const cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return e;
-      kernel<<<kSms, threads, smem, s>>>(q);
-      return cudaGetLastError();
+      return launch_overlapped(kernel, dim3(kSms), threads, smem, s, q);
     }
   }
   const int64_t turns = (static_cast<int64_t>(a.T) + a.rows - 1) / a.rows;
   const int threads = a.tpr * a.rows;
-  block_norm_kernel<RES32, ACT32, VPT, 0><<<static_cast<unsigned>(turns), threads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(block_norm_kernel<RES32, ACT32, VPT, 0>, dim3(static_cast<unsigned>(turns)), threads, 0, s, a);
 }
 template <int VPT>
 cudaError_t launch_forward(const NormArgs& a, bool res32, bool act32, cudaStream_t s) {
@@ -764,8 +769,7 @@ cudaError_t launch_backward_typed(const NormGradArgs& a, unsigned grid, cudaStre
       const cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return e;
-      kernel<<<grid, threads, smem, s>>>(a);
-      return cudaGetLastError();
+      return launch_overlapped(kernel, dim3(grid), threads, smem, s, a);
     }
   }
   const size_t smem = VPT > 2 ? sizeof(float) * 2 * a.d : 0;
@@ -775,8 +779,7 @@ cudaError_t launch_backward_typed(const NormGradArgs& a, unsigned grid, cudaStre
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  block_norm_backward_kernel<RES32, ACT32, VPT, 0><<<grid, threads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(block_norm_backward_kernel<RES32, ACT32, VPT, 0>, dim3(grid), threads, smem, s, a);
 }
 template <int VPT>
 cudaError_t launch_backward(const NormGradArgs& a, bool res32, bool act32, unsigned grid, cudaStream_t s) {
@@ -884,8 +887,7 @@ moe_status moe_block_norm_backward(const moe_norm_config* cfg, const void* r_out
   }
   float* dgc = cfg->gate == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
   if (a.want_pre || a.want_branch) {
-    sum_parts_kernel<<<dim3((a.d + 31) / 32, 2), 256, 0, stream>>>(a, dw_pre, dw_post, dgc);
-    return ok_or_cuda(cudaGetLastError());
+    return ok_or_cuda(launch_overlapped(sum_parts_kernel, dim3((a.d + 31) / 32, 2), 256, 0, stream, a, dw_pre, dw_post, dgc));
   }
   return MOE_OK;
 }

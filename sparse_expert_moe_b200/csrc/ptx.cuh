@@ -529,6 +529,14 @@ __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ---------------------------------------------------------------- overlapped launches
+// A kernel launched to overlap the one before it in its stream may start while that one's last
+// CTAs still run.  wait: until all of that kernel's writes are visible; nothing may be read or
+// written in global memory before.  begin_next: the next kernel's CTAs may take what is free; it
+// stands behind the wait, so that at most two kernels of a stream are under way.
+__device__ __forceinline__ void launch_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_begin_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // ---------------------------------------------------------------- CTA pairs (cta_group::2)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;

@@ -192,3 +192,70 @@ def test_most_groups(op, rows):
         # each of the inner + inner / 16 addends cut at 2^-23 of the largest; two scales: 3 roundings
         tol = ((inner + inner / 16 + 16) * 2.0 ** -23 + 3 * 2.0 ** -24) * mag + 2.0 ** -24 * ref.abs()
         assert (((have.double() - ref).abs() <= tol) | (torch.isnan(have) & torch.isnan(ref))).all(), g
+
+
+# ------------------------------------------------------------------------------------ order
+def test_each_call_waits_for_what_stands_before_it():
+    """Launches overlap the kernel before them in the stream: what that one wrote is there all the
+    same, behind copies, fills, kernels of others and work joined from another stream, eagerly and
+    in a captured graph."""
+    T, n, k = 300, 512, 2048
+    x0, r0 = randn(1, T, k), randn(2, T, k)
+    x1, r1 = randn(3, T, k), randn(4, T, k)
+    w, w1, wn = randn(5, 1, n, k), randn(6, 1, k, n), randn(7, k)
+    ncfg = moe.make_norm_config(T, k)
+    pcfg, qcfg = moe.make_product_config(1, T, n, k), moe.make_product_config(1, T, k, n)
+    ws, ws2 = product_ws(pcfg), product_ws(qcfg)
+    x, r, h, y, z, out = (torch.empty(T, c, device=DEV, dtype=BF) for c in (k, k, k, n, k, k))
+    side = torch.cuda.Stream()
+
+    def chain(x_in, r_in):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            r.copy_(r_in)                        # a copy on another stream
+        x.zero_()                                # a fill
+        x.copy_(x_in)
+        torch.cuda.current_stream().wait_stream(side)
+        moe.moe_block_norm(ncfg, r, x, wn, None, wn, None, h, None)
+        moe.moe_grouped_gemm(pcfg, None, h, None, w, None, y, ws)
+        moe.moe_grouped_gemm(qcfg, None, y, None, w1, None, z, ws2)
+        z.mul_(2.0 ** -11)                       # somebody else's kernel
+        moe.moe_block_norm(ncfg, r, z, wn, None, wn, r, out, None)
+        h.zero_()                                # behind the last reader
+        return out
+
+    def apart(x_in, r_in):
+        """The same calls with the GPU idle between them."""
+        torch.cuda.synchronize()
+        a, b, c, d, e = (torch.empty_like(t) for t in (h, y, z, r, out))
+        moe.moe_block_norm(ncfg, r_in, x_in, wn, None, wn, None, a, None)
+        torch.cuda.synchronize()
+        moe.moe_grouped_gemm(pcfg, None, a, None, w, None, b, ws)
+        torch.cuda.synchronize()
+        moe.moe_grouped_gemm(qcfg, None, b, None, w1, None, c, ws2)
+        torch.cuda.synchronize()
+        c.mul_(2.0 ** -11)
+        torch.cuda.synchronize()
+        moe.moe_block_norm(ncfg, r_in, c, wn, None, wn, d, e, None)
+        torch.cuda.synchronize()
+        return e
+    want = apart(x0, r0), apart(x1, r1)
+    for _ in range(20):
+        for args, e in zip(((x0, r0), (x1, r1)), want):
+            assert torch.equal(chain(*args), e)
+    xs, rs = x0.clone(), r0.clone()
+    warm = torch.cuda.Stream()
+    with torch.cuda.stream(warm):
+        chain(xs, rs)
+    warm.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            chain(xs, rs)
+    for _ in range(5):
+        for args, e in zip(((x0, r0), (x1, r1)), want):
+            xs.copy_(args[0])
+            rs.copy_(args[1])
+            graph.replay()
+            assert torch.equal(out, e)
+    assert moe.moe_read_device_status(ws) == 0 and moe.moe_read_device_status(ws2) == 0
