@@ -384,7 +384,7 @@ struct NormGradArgs {
 // and writes them at the end as one partial per row slot.
 //
 // Measured at T = 4095, d = 7168, bf16, both norms, channel gate, all gradients (352 MB): 67 us
-// with the sum of the partials, 5.0 TB/s, 0.77 of the measured copy bandwidth; bound by
+// with the sum of the partials, 5.2 TB/s, 0.80 of the measured copy bandwidth; bound by
 // instructions (about 45 per element) and the shared-memory reads of the three passes.
 template <bool RES32, bool ACT32, int VPT, int kStages, bool kAll = false>
 __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGradArgs p) {
