@@ -189,18 +189,21 @@ struct Piece {
 
 // Stream kernel: the K blocks of all tiles as one sequence, cut into equal pieces, one per CTA --
 // or, where there are fewer than half as many tiles as CTAs, every tile cut into the same number
-// of parts, one per CTA, so that no CTA has to join two tiles.  Two K blocks at least either way.
+// of parts, one per CTA, so that no CTA has to join two tiles.  Such a part has min_kb K blocks at
+// least, 512 inner elements: with fewer the join of more parts costs more than it saves (one row,
+// n = 512, k = 7168: bf16 19.1 us with parts of 2 blocks, 12.9 of 4, 11.3 of 8, 12.5 of 16; n = 7168,
+// k = 2048, e4m3 10.1 us with 2 or 3, 9.6 with 4, 10.4 with 8).
 struct EvenShare {
   int kb, sharers, parts;       // parts > 0: of every tile
   long long total, u, u1;
 
-  __device__ __forceinline__ EvenShare(int me, int n, int n_tiles, int kb_) : kb(kb_) {
+  __device__ __forceinline__ EvenShare(int me, int n, int n_tiles, int kb_, int min_kb) : kb(kb_) {
     total = static_cast<long long>(n_tiles) * kb;
     sharers = (total + 1) / 2 < n ? static_cast<int>((total + 1) / 2) : n;
     parts = 0;
     u = u1 = 0;
     if (n_tiles > 0 && 2 * n_tiles <= n) {
-      parts = max(1, min(n / n_tiles, kb / 2));
+      parts = max(1, min(n / n_tiles, kb / min_kb));
       if (me < n_tiles * parts) {
         const long long b = static_cast<long long>(me / parts) * kb;
         u = b + kb * (me % parts) / parts;
@@ -422,7 +425,7 @@ __device__ __forceinline__ void join_parts(float* v, Slot slot, int first, int l
 //
 // Measured: 64 groups, n = 7168, k = 2048, 512 rows: 6.43 TB/s (0.98 of a copy); one token's 8
 // groups of n = 4096, k = 7168 78 us (6.0 TB/s: about 6 us are the start, first loads and the
-// join of the cut tiles).  One e4m3 token, n = 7168, k = 2048: 10.0 us, latency: the start of
+// join of the cut tiles).  One e4m3 token, n = 7168, k = 2048: 9.6 us, latency: the start of
 // the CTA and its first loads, three K blocks, the join of the parts.
 template <bool F8, int OP>
 struct StreamCfg {
@@ -495,7 +498,7 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  EvenShare sched(blockIdx.x, gridDim.x, n_tiles, p.k_blocks);
+  EvenShare sched(blockIdx.x, gridDim.x, n_tiles, p.k_blocks, F8 ? 4 : 8);
   Piece c;
 
   if (warp == 0) {
