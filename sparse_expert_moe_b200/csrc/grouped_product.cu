@@ -1451,11 +1451,15 @@ moe_status launch_product(const ProductArgs& a, bool f32, bool stream_tiles, cud
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// Groups of few rows go to the stream kernel (only the average is known on the host): one group
-// of at most a tile, or at most eight rows on average, where few groups hold more than a tile.
-// Measured with 64 groups, n = 7168, k = 2048: 8 rows on average 6.43 TB/s, 16 rows 5.7 (groups
-// above 32 rows read their weights twice), against 6.3 with 32 rows in the pair kernel.
-bool few_rows(const moe_product_config& c) { return c.n_rows <= 32 || c.n_rows <= 8 * c.n_groups; }
+// Groups of few rows go to the stream kernel (only the average is known on the host): at most 32
+// rows in all (e4m3: 64, two tiles' rows), or at most eight per group on average, where few groups
+// hold more than a tile.  Measured with 64 groups, n = 7168, k = 2048: 8 rows on average 6.43 TB/s, 16
+// rows 5.7 (groups above 32 rows read their weights twice), against 6.3 with 32 rows in the pair
+// kernel.  One group of 64 rows, n = 4096, k = 7168: e4m3 16.5 us here, 21.8 in the fold kernel (96
+// rows, n = 7168, k = 2048: 17.0 against 15.7); bf16 19.8 us here, 17.6 in the pair kernel.
+bool few_rows(const moe_product_config& c) {
+  return c.n_rows <= (c.in == MOE_BF16 ? 32 : 64) || c.n_rows <= 8 * c.n_groups;
+}
 
 moe_status common_checks(const moe_product_config* cfg, const int32_t* offsets, const void* x, const void* y,
                          const void* z, const void* ws, size_t ws_bytes) {

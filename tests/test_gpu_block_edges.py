@@ -259,3 +259,20 @@ def test_each_call_waits_for_what_stands_before_it():
             graph.replay()
             assert torch.equal(out, e)
     assert moe.moe_read_device_status(ws) == 0 and moe.moe_read_device_status(ws2) == 0
+
+
+@pytest.mark.parametrize("rows", [33, 64, 65, 96, 128, 129])
+def test_block_scaled_product_between_its_kernels(rows):
+    """Row counts on both sides of the choice of kernel, against sums in 64 bits."""
+    n, k = 264, 2064
+    many = product("fp8", [rows], n, k, out="f32")
+    x, w = randn(1, rows, k), randn(2, 1, n, k)
+    q, v = (100 * x.float()).to(torch.float8_e4m3fn), (100 * w.float()).to(torch.float8_e4m3fn)
+    kb = -(-k // 128)
+    s, t = randn(6, rows, kb).float(), randn(7, 1, -(-n // 128), kb).float()
+    a = q.double() * s.double().repeat_interleave(128, 1)[:, :k]
+    b = v[0].double() * t[0].double().repeat_interleave(128, 1)[:, :k].repeat_interleave(128, 0)[:n]
+    ref, mag = a @ b.T, a.abs() @ b.abs().T
+    # 128 products and 8 steps per block cut at 2^-23 of the largest; kb blocks and scales round
+    tol = ((128 + 8 + 16) * 2.0 ** -23 + (kb + 2) * 2.0 ** -24) * mag + 2.0 ** -24 * ref.abs()
+    assert (((many.double() - ref).abs() <= tol) | (torch.isnan(many) & torch.isnan(ref))).all()
