@@ -31,6 +31,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -45,6 +46,17 @@ constexpr uint32_t kBox = 64 * 128;             // one 64-row box of 128-byte ro
 constexpr uint32_t kTileA = 2 * kBox;           // 128 x 128 bytes
 constexpr int kCounterWord0 = 16;               // header words 16..63: four 8-bit counters each
 constexpr int kMaxCounters = 192;
+// fp32 outputs: K blocks that the tensor cores sum before the sum is added to fp32 registers.  They
+// cut each addend at 2^-23 of the largest, which leaves a sum about 1.1e-9 of its value short per
+// element (7.9e-6 at 7168); sums of 512 elements added in fp32 are off by 6e-7 whatever the length.
+// A bf16 output does not show it and is summed in one go.
+constexpr int kFoldBlocks = 8;
+template <typename OUT>
+constexpr bool kFolds = sizeof(OUT) == 4;
+// Eight epilogue warps that keep 128 sums and 32 products per thread (pair kernel with fp32 output,
+// fold kernel): registers move from warps 0..3 to 4..11, 384 x 168 at launch = 128 x 40 + 256 x 232.
+constexpr int kRegsLow = 40, kRegsHigh = 232;
+
 constexpr int kScaleBlocks = 8;                 // stream kernel: K blocks of scales fetched at a time
 
 struct ProductArgs {
@@ -492,6 +504,7 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
   }
   launch_wait();
   launch_begin_next();
+  constexpr int kRun = F8 ? 1 : (kFolds<OUT> ? kFoldBlocks : 1 << 30);   // K blocks per accumulator
   const int m_blocks = (p.m_total + 128 * C::kMB - 1) / (128 * C::kMB);
   const int n_tiles = build_groups(p, gt, C::kNTok, 16, 1, m_blocks, 0);
   tc_fence_before();
@@ -550,7 +563,8 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
                                 : (idesc_bf16_f32(128, n_pad) | (OP == kNN ? kIdescAMajorMN : 0u));
       uint32_t d0 = 0, b = 0;
       for (int kb = c.kb0; kb < c.kb1; ++kb) {
-        if (F8 || kb == c.kb0) {                // a fresh accumulator buffer
+        const int at = (kb - c.kb0) % kRun;
+        if (at == 0) {                          // a fresh accumulator buffer
           b = it % C::kBufs;
           ok = mbar_poll_warp(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status);
           if (!ok) break;
@@ -565,7 +579,7 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t bd = umma_desc_sw128(sb + kk * 32);
-            const uint32_t accumulate = (kk || (!F8 && kb > c.kb0)) ? 1u : 0u;
+            const uint32_t accumulate = (kk || at) ? 1u : 0u;
 #pragma unroll
             for (int j = 0; j < C::kMB; ++j) {
               const uint32_t aj = sa + j * kTileA;
@@ -575,7 +589,7 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
             }
           }
           umma_commit(&empty_bar[stage]);
-          if (F8 || kb + 1 == c.kb1) umma_commit(&tfull_bar[b]);
+          if (at == kRun - 1 || kb + 1 == c.kb1) umma_commit(&tfull_bar[b]);
         }
         __syncwarp();
         if (++stage == C::kStages) {
@@ -629,11 +643,11 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
     while (ok && sched.next(c)) {
       const Tile t = token_tile(gt, c.tile, C::kNTok, 16, m_blocks, 1);
       float acc[C::kMB][2][16];
+#pragma unroll
+      for (int j = 0; j < C::kMB; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[j][0][i] = acc[j][1][i] = 0.f;
       if (F8) {
-#pragma unroll
-        for (int j = 0; j < C::kMB; ++j)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[j][0][i] = acc[j][1][i] = 0.f;
         for (int kb = c.kb0; kb < c.kb1; ++kb, ++it) {
           const uint32_t b = it % C::kBufs;
           const int q = (kb - c.kb0) % kScaleBlocks;
@@ -664,19 +678,28 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
         }
         if (!ok) break;
       } else {
-        const uint32_t b = it % C::kBufs;
-        if (!mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status)) break;
-        tc_fence_after();
-        const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
+        for (int kb = c.kb0; kb < c.kb1; kb = c.kb1 - kb > kRun ? kb + kRun : c.kb1, ++it) {
+          const uint32_t b = it % C::kBufs;
+          ok = mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
 #pragma unroll
-        for (int j = 0; j < C::kMB; ++j) {
-          if (t.rows > 16) tmem_ld16x2(tb + j * C::kNTok, tb + j * C::kNTok + 16, acc[j][0], acc[j][1]);
-          else tmem_ld16(tb + j * C::kNTok, acc[j][0]);
+          for (int j = 0; j < C::kMB; ++j) {
+            float v0[16], v1[16];
+            if (t.rows > 16) tmem_ld16x2(tb + j * C::kNTok, tb + j * C::kNTok + 16, v0, v1);
+            else tmem_ld16(tb + j * C::kNTok, v0);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[j][0][i] += v0[i];
+            if (t.rows > 16)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[j][1][i] += v1[i];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty_bar[b]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty_bar[b]);
-        ++it;
+        if (!ok) break;
       }
       if (sched.cut(c)) {
         int first, last;
@@ -724,23 +747,28 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
 // tiles in L2; the K blocks of a partial last round are cut.  Two accumulators take turns, so the
 // epilogue of a tile runs under the next tile's MMAs.
 //
-// Measured: one group of 8192 rows, n = 4096, k = 7168: 320 us for NT and TN (1500 TFLOP/s), 370
-// for NN; one K block takes 513 cycles, of which the MMAs need 512, and the 1000 W power limit
-// holds the clock near 1.2 GHz in a loop of them.  TN of 32 groups x 256 rows, n = 7168, k = 2048,
-// fp32: 388 us, 4.8 TB/s of stores; a tile has four K blocks there for 256 KB of sums, so the
-// stores bound it.  Eight epilogue warps measured 394 us.
+// With fp32 output (FOLD) an accumulator holds kFoldBlocks K blocks, and eight epilogue warps add
+// them up in registers, 128 columns per thread, under the MMAs of the next.
+//
+// Measured: one group of 8192 rows, n = 4096, k = 7168: 306-320 us for NT and TN (1500 TFLOP/s),
+// 370 for NN; one K block takes 513 cycles, of which the MMAs need 512, and the 1000 W power limit
+// holds the clock near 1.2 GHz in a loop of them.  fp32: NT 324 us (one accumulator for the whole sum
+// 328), NN 390 (375), TN 440 (375).  TN of 32 groups x 256 rows, n = 7168, k = 2048, fp32: 462-480
+// us on a GPU where four epilogue warps and one accumulator took 510, 390 on another; a tile has
+// four K blocks there for 256 KB of sums, so the stores bound it.
 constexpr size_t kPartFloats = 128 * 256;       // a CTA's sums of a cut tile
 
-template <int OP>
+template <int OP, bool FOLD>
 struct PairCfg {
   static constexpr int kWidth = 256;                              // tokens (TN: columns) per tile
   static constexpr uint32_t kStage = 2 * kTileA;                  // 128 rows of either operand
   static constexpr int kStages = OP == kTN ? 5 : 6;
   static constexpr int kBufs = 2;                                 // accumulators of 256 columns
   static constexpr int kCols = 256;
-  static constexpr int kEpi = 4, kEpi0 = 3;                       // epilogue warps, the first of them
+  static constexpr int kEpi = FOLD ? 8 : 4, kEpi0 = FOLD ? 4 : 3; // epilogue warps, the first of them
   static constexpr int kThreads = 32 * (kEpi0 + kEpi);
-  static constexpr uint32_t kWarpStage = OP == kTN ? 2 * 4096 : 2048;
+  static constexpr int kBoxes = FOLD ? 1 : 2;                     // TN: stages of 4 KB per warp
+  static constexpr uint32_t kWarpStage = OP == kTN ? kBoxes * 4096 : 2048;
   static constexpr uint32_t kStaging = kEpi * kWarpStage;
   static constexpr uint32_t kSmem =
       1024 + kStages * kStage + 1024 + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
@@ -754,9 +782,11 @@ __device__ __forceinline__ bool ragged_block(int rows, int kb) {
 }
 
 template <int OP, typename OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP, kFolds<OUT>>::kThreads, 1)
     pair_kernel(const __grid_constant__ ProductArgs p) {
-  using C = PairCfg<OP>;
+  constexpr bool kFold = kFolds<OUT>;
+  constexpr int kRun = kFold ? kFoldBlocks : 1 << 30;  // K blocks per accumulator
+  using C = PairCfg<OP, kFold>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -825,104 +855,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
   auto grad_cols = [&]() { return min(256, p.n_total - t.nb * 256); };
   auto grad_n = [&]() { return grad_cols() > 128 ? 256 : 128; };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- TMA producer (both CTAs)
-    const bool elected = elect_one();
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    while (ok && fetch()) {
-      const int m0 = t.mb * 256 + rank * 128;
-      for (int kb = c.kb0; kb < c.kb1; ++kb) {
-        ok = mbar_poll_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
-        if (!ok) break;
-        uint8_t* st = tiles + stage * C::kStage;
-        uint8_t* bt = st + kTileA;
-        if (OP == kTN) {
-          // loads count on the leader's barrier, which the leader's producer arrives on twice;
-          // those of a ragged last block count on this CTA's own, and the CTAs' zeroing warps
-          // arrive on the leader's, once each, when its rows are in order
-          const int half = grad_n() / 2;                          // columns per CTA: 64 or 128
-          const int y = t.row0 + kb * 64, x0 = t.nb * 256 + rank * half;
-          const bool ragged = ragged_block(t.rows, kb);
-          const uint32_t bytes = kTileA + half * 128;
-          const uint32_t bar = mapa_shared(ragged ? &land_bar[stage] : &full_bar[stage], ragged ? rank : 0);
-          if (elected) {
-            if (ragged) {
-              mbar_arrive_expect_tx(&land_bar[stage], bytes);
-            } else if (leader) {
-              mbar_arrive(&full_bar[stage]);
-              mbar_arrive_expect_tx(&full_bar[stage], 2 * bytes);
-            }
-            tma_load_2d_pair(st, &p.wmap, bar, m0, y);
-            tma_load_2d_pair(st + kBox, &p.wmap, bar, m0 + 64, y);
-            tma_load_2d_pair(bt, &p.tmap[0], bar, x0, y);
-            if (half > 64) tma_load_2d_pair(bt + kBox, &p.tmap[0], bar, x0 + 64, y);
-          }
-        } else {
-          const uint32_t bar = mapa_shared(&full_bar[stage], 0);
-          const int kx = kb * 64;
-          const int n_pad = (t.rows + 31) & ~31;
-          // this CTA's half of the token rows, in boxes of 128, 64, 32 and 16 rows
-          const int rows = n_pad / 2, y = t.row0 + rank * rows;
-          if (elected) {
-            if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kTileA + n_pad * 128);
-            if (OP == kNT) {
-              tma_load_3d_pair(st, &p.wmap, bar, kx, m0, t.g);
-            } else {
-              tma_load_3d_pair(st, &p.wmap, bar, m0, kx, t.g);
-              tma_load_3d_pair(st + kBox, &p.wmap, bar, m0 + 64, kx, t.g);
-            }
-            for (int bi = 0, off = 0; bi < 4; ++bi) {
-              const int box = 128 >> bi;
-              while (rows - off >= box) {
-                tma_load_2d_pair(bt + off * 128, &p.tmap[bi], bar, kx, y + off);
-                off += box;
-              }
-            }
-          }
-        }
-        __syncwarp();
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer (the leader)
-    if (leader) {
+  if (warp < C::kEpi0) {
+    if constexpr (kFold) regs_down<kRegsLow>();   // (one instruction for the whole warpgroup)
+    if (warp == 0) {
+      // ---------------------------------------------------------- TMA producer (both CTAs)
       const bool elected = elect_one();
       int stage = 0;
-      uint32_t phase = 0, it = 0;                // accumulators used so far
+      uint32_t phase = 0;
       bool ok = true;
       while (ok && fetch()) {
-        if (c.kb1 <= c.kb0) continue;                             // TN: a group without rows
-        const uint32_t b = it % C::kBufs;
-        if (!mbar_poll_warp(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status)) break;
-        ++it;
-        const int n_pad = OP == kTN ? grad_n() : (t.rows + 31) & ~31;
-        const uint32_t idesc = idesc_bf16_f32(256, n_pad) | (OP != kNT ? kIdescAMajorMN : 0u) |
-                               (OP == kTN ? kIdescBMajorMN : 0u);
-        const uint32_t d = tmem + b * C::kCols;
+        const int m0 = t.mb * 256 + rank * 128;
         for (int kb = c.kb0; kb < c.kb1; ++kb) {
-          ok = OP == kTN && ragged_block(t.rows, kb)
-                   ? __all_sync(0xffffffffu, mbar_wait_cluster(&full_bar[stage], phase, abort_flag, status)) != 0
-                   : mbar_poll_warp(&full_bar[stage], phase, abort_flag, status);
+          ok = mbar_poll_warp(&empty_bar[stage], phase ^ 1u, abort_flag, status);
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t sa = smem_u32(tiles) + stage * C::kStage, sb = sa + kTileA;
-          const int left = OP == kTN ? t.rows - kb * 64 : 64;
-          if (elected) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              if (OP == kTN && kk * 16 >= left) break;
-              const uint64_t ad = OP == kNT ? umma_desc_sw128(sa + kk * 32) : umma_desc_mn_sw128(sa + kk * 2048);
-              const uint64_t bd = OP == kTN ? umma_desc_mn_sw128(sb + kk * 2048) : umma_desc_sw128(sb + kk * 32);
-              umma_bf16_pair(d, ad, bd, idesc, (kb > c.kb0 || kk) ? 1u : 0u);
+          uint8_t* st = tiles + stage * C::kStage;
+          uint8_t* bt = st + kTileA;
+          if (OP == kTN) {
+            // loads count on the leader's barrier, which the leader's producer arrives on twice;
+            // those of a ragged last block count on this CTA's own, and the CTAs' zeroing warps
+            // arrive on the leader's, once each, when its rows are in order
+            const int half = grad_n() / 2;                          // columns per CTA: 64 or 128
+            const int y = t.row0 + kb * 64, x0 = t.nb * 256 + rank * half;
+            const bool ragged = ragged_block(t.rows, kb);
+            const uint32_t bytes = kTileA + half * 128;
+            const uint32_t bar = mapa_shared(ragged ? &land_bar[stage] : &full_bar[stage], ragged ? rank : 0);
+            if (elected) {
+              if (ragged) {
+                mbar_arrive_expect_tx(&land_bar[stage], bytes);
+              } else if (leader) {
+                mbar_arrive(&full_bar[stage]);
+                mbar_arrive_expect_tx(&full_bar[stage], 2 * bytes);
+              }
+              tma_load_2d_pair(st, &p.wmap, bar, m0, y);
+              tma_load_2d_pair(st + kBox, &p.wmap, bar, m0 + 64, y);
+              tma_load_2d_pair(bt, &p.tmap[0], bar, x0, y);
+              if (half > 64) tma_load_2d_pair(bt + kBox, &p.tmap[0], bar, x0 + 64, y);
             }
-            umma_commit_pair(&empty_bar[stage], 0x3);
-            if (kb + 1 == c.kb1) umma_commit_pair(&tfull_bar[b], 0x3);
+          } else {
+            const uint32_t bar = mapa_shared(&full_bar[stage], 0);
+            const int kx = kb * 64;
+            const int n_pad = (t.rows + 31) & ~31;
+            // this CTA's half of the token rows, in boxes of 128, 64, 32 and 16 rows
+            const int rows = n_pad / 2, y = t.row0 + rank * rows;
+            if (elected) {
+              if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * kTileA + n_pad * 128);
+              if (OP == kNT) {
+                tma_load_3d_pair(st, &p.wmap, bar, kx, m0, t.g);
+              } else {
+                tma_load_3d_pair(st, &p.wmap, bar, m0, kx, t.g);
+                tma_load_3d_pair(st + kBox, &p.wmap, bar, m0 + 64, kx, t.g);
+              }
+              for (int bi = 0, off = 0; bi < 4; ++bi) {
+                const int box = 128 >> bi;
+                while (rows - off >= box) {
+                  tma_load_2d_pair(bt + off * 128, &p.tmap[bi], bar, kx, y + off);
+                  off += box;
+                }
+              }
+            }
           }
           __syncwarp();
           if (++stage == C::kStages) {
@@ -931,42 +921,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
           }
         }
       }
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    if (OP == kTN) {
-      // -------------------------------------------------------- rows behind the group's last
-      // The last K block's rows past the group belong to the next group (or to nobody): in both
-      // operands they are overwritten with zeros up to the MMA's 16-row step.
-      int stage = 0;
-      uint32_t parity = 0;                       // bit s: phase of land_bar[s]
-      bool ok = true;
-      while (ok && fetch()) {
-        const int boxes = 2 + grad_n() / 128;
-        for (int kb = c.kb0; kb < c.kb1; ++kb, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
-          if (!ragged_block(t.rows, kb)) continue;
-          ok = mbar_poll_warp(&land_bar[stage], (parity >> stage) & 1u, abort_flag, status);
-          if (!ok) break;
-          parity ^= 1u << stage;
-          const int left = t.rows - kb * 64;
-          uint8_t* st = tiles + stage * C::kStage;
-          const int units = (16 - (left & 15)) * 8;               // 16-byte pieces per box
-          for (int i = lane; i < units * boxes; i += 32) {
-            const int box = i / units;
-            *reinterpret_cast<uint4*>(st + box * kBox + left * 128 + (i - box * units) * 16) =
-                make_uint4(0, 0, 0, 0);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------- MMA issuer (the leader)
+      if (leader) {
+        const bool elected = elect_one();
+        int stage = 0;
+        uint32_t phase = 0, it = 0;                // accumulators used so far
+        bool ok = true;
+        while (ok && fetch()) {
+          if (c.kb1 <= c.kb0) continue;                             // TN: a group without rows
+          const int n_pad = OP == kTN ? grad_n() : (t.rows + 31) & ~31;
+          const uint32_t idesc = idesc_bf16_f32(256, n_pad) | (OP != kNT ? kIdescAMajorMN : 0u) |
+                                 (OP == kTN ? kIdescBMajorMN : 0u);
+          uint32_t b = 0;
+          for (int kb = c.kb0; kb < c.kb1; ++kb) {
+            const int at = (kb - c.kb0) % kRun;
+            if (at == 0) {                       // a fresh accumulator
+              b = it % C::kBufs;
+              ok = mbar_poll_warp(&tempty_bar[b], ((it / C::kBufs) & 1u) ^ 1u, abort_flag, status);
+              if (!ok) break;
+              ++it;
+            }
+            const uint32_t d = tmem + b * C::kCols;
+            ok = OP == kTN && ragged_block(t.rows, kb)
+                     ? __all_sync(0xffffffffu, mbar_wait_cluster(&full_bar[stage], phase, abort_flag, status)) != 0
+                     : mbar_poll_warp(&full_bar[stage], phase, abort_flag, status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t sa = smem_u32(tiles) + stage * C::kStage, sb = sa + kTileA;
+            const int left = OP == kTN ? t.rows - kb * 64 : 64;
+            if (elected) {
+  #pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                if (OP == kTN && kk * 16 >= left) break;
+                const uint64_t ad = OP == kNT ? umma_desc_sw128(sa + kk * 32) : umma_desc_mn_sw128(sa + kk * 2048);
+                const uint64_t bd = OP == kTN ? umma_desc_mn_sw128(sb + kk * 2048) : umma_desc_sw128(sb + kk * 32);
+                umma_bf16_pair(d, ad, bd, idesc, (at || kk) ? 1u : 0u);
+              }
+              umma_commit_pair(&empty_bar[stage], 0x3);
+              if (at == kRun - 1 || kb + 1 == c.kb1) umma_commit_pair(&tfull_bar[b], 0x3);
+            }
+            __syncwarp();
+            if (++stage == C::kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(&full_bar[stage], 0));
         }
       }
+      __syncwarp();
+    } else if (warp == 2) {
+      if (OP == kTN) {
+        // -------------------------------------------------------- rows behind the group's last
+        // The last K block's rows past the group belong to the next group (or to nobody): in both
+        // operands they are overwritten with zeros up to the MMA's 16-row step.
+        int stage = 0;
+        uint32_t parity = 0;                       // bit s: phase of land_bar[s]
+        bool ok = true;
+        while (ok && fetch()) {
+          const int boxes = 2 + grad_n() / 128;
+          for (int kb = c.kb0; kb < c.kb1; ++kb, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
+            if (!ragged_block(t.rows, kb)) continue;
+            ok = mbar_poll_warp(&land_bar[stage], (parity >> stage) & 1u, abort_flag, status);
+            if (!ok) break;
+            parity ^= 1u << stage;
+            const int left = t.rows - kb * 64;
+            uint8_t* st = tiles + stage * C::kStage;
+            const int units = (16 - (left & 15)) * 8;               // 16-byte pieces per box
+            for (int i = lane; i < units * boxes; i += 32) {
+              const int box = i / units;
+              *reinterpret_cast<uint4*>(st + box * kBox + left * 128 + (i - box * units) * 16) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa_shared(&full_bar[stage], 0));
+          }
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------- epilogue (both CTAs)
+    if constexpr (kFold) regs_up<kRegsHigh>();
     const int sub = warp & 3;                    // TMEM lane quadrant
     const int m_local = sub * 32 + lane;
+    const int from = kFold ? ((warp - C::kEpi0) >> 2) * 128 : 0;   // kFold: the warp's 128 columns
     uint8_t* stg = staging + (warp - C::kEpi0) * C::kWarpStage;
     EpilogueSync sync{epi_bar, abort_flag, status};
     uint32_t it = 0, stores = 0;
@@ -979,6 +1019,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
     while (ok && fetch()) {
       const int m0 = t.mb * 256 + rank * 128 + sub * 32;          // the warp's first output index
       const int cols = OP == kTN ? grad_cols() : t.rows;          // TMEM columns in use
+      const int to = kFold ? min(cols, from + 128) : cols;
       int first = 0, last = 0;
       if (cut) sched.owners(c.tile, first, last);
       auto slot = [&](int owner) {
@@ -1004,67 +1045,115 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
           for (int i = 0; i < 16; i += 4) write_part(mine, n0 + i, v + i);
         }
       };
-      if (OP == kTN && !cut) {
-        // 32 rows x 128 bytes at a time through a swizzled stage (two, in turn) and a TMA store,
-        // which leaves out what lies past n and k
-        constexpr int kStep = 128 / static_cast<int>(sizeof(OUT));
-        const bool rows = c.kb1 > c.kb0;         // false: a group without rows, zeros
-        uint32_t tb = 0;
-        if (rows) {
-          const uint32_t b = it % C::kBufs;
-          if (!mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status)) break;
-          tc_fence_after();
-          tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
-        }
-        for (int n0 = 0; n0 < cols; n0 += kStep) {
-          float v[kStep];
-          if (rows) {
-            if constexpr (kStep == 32) tmem_ld32(tb + n0, v);
-            else tmem_ld64(tb + n0, v);
+      // TN: 32 rows x 128 bytes through a swizzled stage and a TMA store, which leaves out what
+      // lies past n and k
+      constexpr int kStep = 128 / static_cast<int>(sizeof(OUT));
+      auto box_out = [&](const float* v, int n0) {
+        uint8_t* box = stg + stores % C::kBoxes * 4096;
+        if (lane == 0) bulk_wait_read<C::kBoxes - 1>();           // an earlier store has left this stage
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          uint4 q;
+          if constexpr (kStep == 32) {
+            q = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
+                           __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
           } else {
+            __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
 #pragma unroll
-            for (int i = 0; i < kStep; ++i) v[i] = 0.f;
+            for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]);
           }
-          uint8_t* box = stg + (stores & 1) * 4096;
-          if (lane == 0) bulk_wait_read<1>();    // the store before last has left this stage
-          __syncwarp();
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            uint4 q;
-            if constexpr (kStep == 32) {
-              q = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]),
-                             __float_as_uint(v[4 * u + 2]), __float_as_uint(v[4 * u + 3]));
-            } else {
-              __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]);
-            }
-            *reinterpret_cast<uint4*>(box + lane * 128 + ((u ^ (lane & 7)) << 4)) = q;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            if (m0 < p.m_total) tma_store_3d(&p.omap, box, t.nb * 256 + n0, m0, t.g);
-            bulk_commit();
-          }
-          ++stores;
+          *reinterpret_cast<uint4*>(box + lane * 128 + ((u ^ (lane & 7)) << 4)) = q;
         }
-        if (rows) {
-          release(it % C::kBufs);
-          ++it;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (m0 < p.m_total) tma_store_3d(&p.omap, box, t.nb * 256 + n0, m0, t.g);
+          bulk_commit();
+        }
+        ++stores;
+      };
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+      if constexpr (kFold) {
+        f32x2 acc[64];                           // the warp's 128 columns
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[i] = both2(0.f);
+        for (int kb = c.kb0; kb < c.kb1; kb += kRun, ++it) {
+          const uint32_t b = it % C::kBufs;
+          ok = mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
+          if (!ok) break;
+          tc_fence_after();
+          if (from < to) {
+            const uint32_t tb = lanes + b * C::kCols + from;
+            uint32_t v[2][16];
+            tmem_ld16_begin(tb, v[0]);
+            tmem_ld_end(v[0]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              if (q < 7) tmem_ld16_begin(tb + (q + 1) * 16, v[(q + 1) & 1]);
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                f32x2& a = acc[(q * 16 + i) / 2];
+                a = add2(a, pack2(v[q & 1][i], v[q & 1][i + 1]));
+              }
+              if (q < 7) tmem_ld_end(v[(q + 1) & 1]);
+            }
+          }
+          release(b);
+        }
+        if (!ok) break;
+        auto sums = [&](int i, float* v, auto n) {
+#pragma unroll
+          for (int e = 0; e < decltype(n)::value / 2; ++e) {
+            const float2 f = unpack2(acc[i / 2 + e]);
+            v[2 * e] = f.x;
+            v[2 * e + 1] = f.y;
+          }
+        };
+        if (OP == kTN && !cut) {
+#pragma unroll
+          for (int i = 0; i < 128; i += 32) {
+            float v[32];
+            sums(i, v, std::integral_constant<int, 32>());
+            if (from + i < to) box_out(v, from + i);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 128; i += 16) {
+            float v[16];
+            sums(i, v, std::integral_constant<int, 16>());
+            if (from + i < to) emit(v, from + i);
+          }
         }
       } else {
-        const uint32_t b = it % C::kBufs;
-        if (!mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status)) break;
-        tc_fence_after();
-        const uint32_t tb = tmem + (static_cast<uint32_t>(sub * 32) << 16) + b * C::kCols;
-        for (int n0 = 0; n0 < cols; n0 += 16) {
-          float v[16];
-          tmem_ld16(tb + n0, v);
-          emit(v, n0);
+        const bool rows = c.kb1 > c.kb0;         // false (TN): a group without rows, zeros
+        const uint32_t b = it % C::kBufs, tb = lanes + b * C::kCols;
+        if (rows) {
+          if (!mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status)) break;
+          tc_fence_after();
         }
-        release(b);
-        ++it;
+        if (OP == kTN && !cut) {
+          for (int n0 = 0; n0 < cols; n0 += 64) {
+            float v[64];
+            if (rows) {
+              tmem_ld64(tb + n0, v);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) v[i] = 0.f;
+            }
+            box_out(v, n0);
+          }
+        } else {
+          for (int n0 = 0; n0 < cols; n0 += 16) {
+            float v[16];
+            tmem_ld16(tb + n0, v);
+            emit(v, n0);
+          }
+        }
+        if (rows) {
+          release(b);
+          ++it;
+        }
       }
       if (!cut) continue;
       if (!arrive_last(p.header, 2 * first + rank, last - first + 1, sync, last_flag,
@@ -1074,7 +1163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
       }
-      for (int n0 = 0; n0 < cols; n0 += 32) {
+      for (int n0 = from; n0 < to; n0 += 32) {
         float v[32];
         join_parts<32, 2>(v, slot, first, last, n0, cols - n0);
         finish(v, n0);
@@ -1117,9 +1206,6 @@ struct FoldCfg {
   static constexpr int kStages = 4;
   static constexpr int kCols = 256;                               // per buffer
   static constexpr int kThreads = 384;
-  // an epilogue thread keeps 128 sums and 32 products: registers move from warps 0..3 to 4..11.
-  // 384 x 168 at launch = 128 x 40 + 256 x 232.
-  static constexpr int kRegsLow = 40, kRegsHigh = 232;
   static constexpr uint32_t kWarpStage = 1024;
   static constexpr uint32_t kStaging = 8 * kWarpStage;
   static constexpr int kRowScales = 128 + 2;                      // per K block: tokens, weight blocks
@@ -1189,7 +1275,7 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
   auto halves = [&]() { return p.m_total - t.mb * 256 > 128 ? 2 : 1; };
 
   if (warp < 4) {
-    regs_down<C::kRegsLow>();                    // (one instruction for the whole warpgroup)
+    regs_down<kRegsLow>();                    // (one instruction for the whole warpgroup)
     if (warp == 0) {
       // -------------------------------------------------------- TMA producer
       const bool elected = elect_one();
@@ -1284,7 +1370,7 @@ __global__ void __launch_bounds__(FoldCfg::kThreads, 1) fold_kernel(const __grid
     }
   } else {
     // ---------------------------------------------------------- epilogue
-    regs_up<C::kRegsHigh>();
+    regs_up<kRegsHigh>();
     const int sub = warp & 3;                    // TMEM lane quadrant: tokens sub * 32 + lane
     const int half = (warp - 4) >> 2;            // 128-column half of the tile
     uint8_t* stg = staging + (warp - 4) * C::kWarpStage;
@@ -1434,6 +1520,7 @@ cudaError_t launch_product_kernel(K kernel, const ProductArgs& a, int grid, int 
 
 template <bool F8, int OP, typename OUT>
 cudaError_t launch_product(const ProductArgs& a, bool stream_tiles, cudaStream_t s) {
+  using Pair = PairCfg<OP, kFolds<OUT>>;
   const int sms = device_sms();
   if (sms < 2) return cudaErrorInvalidDevice;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
@@ -1442,7 +1529,7 @@ cudaError_t launch_product(const ProductArgs& a, bool stream_tiles, cudaStream_t
       return launch_product_kernel(stream_kernel<F8, OP, OUT>, a, ctas, 224, StreamCfg<F8, OP>::kSmem, s);
   }
   if constexpr (F8) return launch_product_kernel(fold_kernel<OUT>, a, ctas, FoldCfg::kThreads, FoldCfg::kSmem, s);
-  else return launch_product_kernel(pair_kernel<OP, OUT>, a, ctas / 2 * 2, PairCfg<OP>::kThreads, PairCfg<OP>::kSmem, s);
+  else return launch_product_kernel(pair_kernel<OP, OUT>, a, ctas / 2 * 2, Pair::kThreads, Pair::kSmem, s);
 }
 template <bool F8, int OP>
 moe_status launch_product(const ProductArgs& a, bool f32, bool stream_tiles, cudaStream_t s) {

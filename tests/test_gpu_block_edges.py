@@ -276,3 +276,30 @@ def test_block_scaled_product_between_its_kernels(rows):
     # 128 products and 8 steps per block cut at 2^-23 of the largest; kb blocks and scales round
     tol = ((128 + 8 + 16) * 2.0 ** -23 + (kb + 2) * 2.0 ** -24) * mag + 2.0 ** -24 * ref.abs()
     assert (((many.double() - ref).abs() <= tol) | (torch.isnan(many) & torch.isnan(ref))).all()
+
+
+@pytest.mark.parametrize("op,rows", [("gemm", 3), ("gemm", 300), ("dgrad", 5), ("dgrad", 260), ("wgrad", 7168)])
+def test_long_sums_in_fp32(op, rows):
+    """fp32 outputs add up sums of 512 products.  All terms positive, so that every cut shows: a step
+    of the tensor cores cuts 16 products and the sum so far, 17 addends, at 2^-23 of the largest, 32
+    steps in a sum of 512, and the 14 sums and up to 4 parts of a cut tile round once each.  One sum
+    of all 7168 would lose about half of 17 * 448 * 2^-23 / 2, 2e-4."""
+    n, k = (264, 7168) if op != "dgrad" else (7168, 264)
+    if op == "wgrad":
+        n, k = 136, 264
+    g = torch.Generator(DEV).manual_seed(3)
+    x = (0.5 + 0.5 * torch.rand(rows, n if op == "dgrad" else k, device=DEV, generator=g)).to(BF)
+    y = (0.5 + 0.5 * torch.rand(*((rows, n) if op == "wgrad" else (1, n, k)), device=DEV, generator=g)).to(BF)
+    cfg = moe.make_product_config(1, rows, n, k, out="f32")
+    ws = product_ws(cfg)
+    if op == "wgrad":
+        out, ref = torch.empty(1, n, k, device=DEV), (y.double().T @ x.double())[None]
+        moe.moe_grouped_gemm_wgrad(cfg, None, y, x, out, ws)
+    elif op == "gemm":
+        out, ref = torch.empty(rows, n, device=DEV), x.double() @ y[0].double().T
+        moe.moe_grouped_gemm(cfg, None, x, None, y, None, out, ws)
+    else:
+        out, ref = torch.empty(rows, k, device=DEV), x.double() @ y[0].double()
+        moe.moe_grouped_gemm_dgrad(cfg, None, x, y, out, ws)
+    tol = (32 * 17 * 2.0 ** -23 + 18 * 2.0 ** -24) * ref
+    assert ((out.double() - ref).abs() <= tol).all(), float(((out.double() - ref).abs() / ref).max())
