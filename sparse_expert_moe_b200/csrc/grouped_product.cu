@@ -46,15 +46,13 @@ constexpr uint32_t kBox = 64 * 128;             // one 64-row box of 128-byte ro
 constexpr uint32_t kTileA = 2 * kBox;           // 128 x 128 bytes
 constexpr int kCounterWord0 = 16;               // header words 16..63: four 8-bit counters each
 constexpr int kMaxCounters = 192;
-// fp32 outputs: K blocks that the tensor cores sum before the sum is added to fp32 registers.  They
+// bf16 operands: K blocks that the tensor cores sum before the sum is added to fp32 registers.  They
 // cut each addend at 2^-23 of the largest, which leaves a sum about 1.1e-9 of its value short per
-// element (7.9e-6 at 7168); sums of 512 elements added in fp32 are off by 6e-7 whatever the length.
-// A bf16 output does not show it and is summed in one go.
+// element (7.9e-6 at 7168, which moves one bf16 rounding in 500); sums of 512 elements are short by
+// 6e-7, and adding them in fp32 rounds once each.
 constexpr int kFoldBlocks = 8;
-template <typename OUT>
-constexpr bool kFolds = sizeof(OUT) == 4;
-// Eight epilogue warps that keep 128 sums and 32 products per thread (pair kernel with fp32 output,
-// fold kernel): registers move from warps 0..3 to 4..11, 384 x 168 at launch = 128 x 40 + 256 x 232.
+// Eight epilogue warps that keep 128 sums and 32 products per thread (pair and fold kernel):
+// registers move from warps 0..3 to 4..11, 384 x 168 at launch = 128 x 40 + 256 x 232.
 constexpr int kRegsLow = 40, kRegsHigh = 232;
 
 constexpr int kScaleBlocks = 8;                 // stream kernel: K blocks of scales fetched at a time
@@ -428,6 +426,26 @@ __device__ __forceinline__ void join_parts(float* v, Slot slot, int first, int l
   }
 }
 
+// acc += the warp's first `cols` of 128 columns in TMEM, 16 at a time, each load under way during the
+// additions of the one before.  (A second form for all 128, without the tests, was 2% slower.)
+__device__ __forceinline__ void add_columns(uint32_t tb, int cols, f32x2 (&acc)[64]) {
+  uint32_t v[2][16];
+  tmem_ld16_begin(tb, v[0]);
+  tmem_ld_end(v[0]);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const bool more = q < 7 && (q + 1) * 16 < cols;
+    if (more) tmem_ld16_begin(tb + (q + 1) * 16, v[(q + 1) & 1]);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      f32x2& a = acc[(q * 16 + i) / 2];
+      a = add2(a, pack2(v[q & 1][i], v[q & 1][i + 1]));
+    }
+    if (!more) break;
+    tmem_ld_end(v[(q + 1) & 1]);
+  }
+}
+
 // ------------------------------------------------------------------ stream kernel
 // Groups of few rows: every weight byte is used for a handful of tokens, so HBM bounds it and the
 // tile is made for a steady stream.  The weights are the M side (256 rows per tile, two MMAs), the
@@ -504,7 +522,7 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
   }
   launch_wait();
   launch_begin_next();
-  constexpr int kRun = F8 ? 1 : (kFolds<OUT> ? kFoldBlocks : 1 << 30);   // K blocks per accumulator
+  constexpr int kRun = F8 ? 1 : kFoldBlocks;     // K blocks per accumulator
   const int m_blocks = (p.m_total + 128 * C::kMB - 1) / (128 * C::kMB);
   const int n_tiles = build_groups(p, gt, C::kNTok, 16, 1, m_blocks, 0);
   tc_fence_before();
@@ -744,31 +762,28 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
 // 128-row tiles.  The weight index is the M side and the group's tokens are the N side in steps of
 // 32, so a short group costs a narrow MMA; TN has the weight's n index on M, its k index on N.
 // Whole rounds of tiles go to the pairs in an order that keeps a few weight blocks and token
-// tiles in L2; the K blocks of a partial last round are cut.  Two accumulators take turns, so the
-// epilogue of a tile runs under the next tile's MMAs.
+// tiles in L2; the K blocks of a partial last round are cut.  Two accumulators of kFoldBlocks K
+// blocks take turns: eight epilogue warps add one up in registers, 128 columns per thread, and
+// store a finished tile, under the MMAs of the next.
 //
-// With fp32 output (FOLD) an accumulator holds kFoldBlocks K blocks, and eight epilogue warps add
-// them up in registers, 128 columns per thread, under the MMAs of the next.
-//
-// Measured: one group of 8192 rows, n = 4096, k = 7168: 306-320 us for NT and TN (1500 TFLOP/s),
-// 370 for NN; one K block takes 513 cycles, of which the MMAs need 512, and the 1000 W power limit
-// holds the clock near 1.2 GHz in a loop of them.  fp32: NT 324 us (one accumulator for the whole sum
-// 328), NN 390 (375), TN 440 (375).  TN of 32 groups x 256 rows, n = 7168, k = 2048, fp32: 462-480
-// us on a GPU where four epilogue warps and one accumulator took 510, 390 on another; a tile has
-// four K blocks there for 256 KB of sums, so the stores bound it.
+// Measured: one group of 8192 rows, n = 4096, k = 7168: 325 us for NT (1480 TFLOP/s), 336 for NN,
+// 350-440 for TN; one K block takes 513 cycles, of which the MMAs need 512, and the 1000 W power limit
+// holds the clock near 1.2 GHz in a loop of them.  fp32 output: 335-357, 370-390 and 430-470.  One
+// accumulator for the whole sum, stored as bf16, took 310, 317 and 335-400.  TN of 32 groups x 256
+// rows, n = 7168, k = 2048, fp32: 460 us; a tile has four K blocks there for 256 KB of sums, so the
+// stores bound it.
 constexpr size_t kPartFloats = 128 * 256;       // a CTA's sums of a cut tile
 
-template <int OP, bool FOLD>
+template <int OP>
 struct PairCfg {
   static constexpr int kWidth = 256;                              // tokens (TN: columns) per tile
   static constexpr uint32_t kStage = 2 * kTileA;                  // 128 rows of either operand
   static constexpr int kStages = OP == kTN ? 5 : 6;
   static constexpr int kBufs = 2;                                 // accumulators of 256 columns
   static constexpr int kCols = 256;
-  static constexpr int kEpi = FOLD ? 8 : 4, kEpi0 = FOLD ? 4 : 3; // epilogue warps, the first of them
+  static constexpr int kEpi = 8, kEpi0 = 4;                       // epilogue warps, the first of them
   static constexpr int kThreads = 32 * (kEpi0 + kEpi);
-  static constexpr int kBoxes = FOLD ? 1 : 2;                     // TN: stages of 4 KB per warp
-  static constexpr uint32_t kWarpStage = OP == kTN ? kBoxes * 4096 : 2048;
+  static constexpr uint32_t kWarpStage = OP == kTN ? 4096 : 2048; // TN: one box of a store
   static constexpr uint32_t kStaging = kEpi * kWarpStage;
   static constexpr uint32_t kSmem =
       1024 + kStages * kStage + 1024 + kStaging + ((sizeof(GroupTable) + 15) & ~15u);
@@ -782,11 +797,10 @@ __device__ __forceinline__ bool ragged_block(int rows, int kb) {
 }
 
 template <int OP, typename OUT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP, kFolds<OUT>>::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThreads, 1)
     pair_kernel(const __grid_constant__ ProductArgs p) {
-  constexpr bool kFold = kFolds<OUT>;
-  constexpr int kRun = kFold ? kFoldBlocks : 1 << 30;  // K blocks per accumulator
-  using C = PairCfg<OP, kFold>;
+  constexpr int kRun = kFoldBlocks;              // K blocks per accumulator
+  using C = PairCfg<OP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -856,7 +870,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP, kFolds<O
   auto grad_n = [&]() { return grad_cols() > 128 ? 256 : 128; };
 
   if (warp < C::kEpi0) {
-    if constexpr (kFold) regs_down<kRegsLow>();   // (one instruction for the whole warpgroup)
+    regs_down<kRegsLow>();                       // (one instruction for the whole warpgroup)
     if (warp == 0) {
       // ---------------------------------------------------------- TMA producer (both CTAs)
       const bool elected = elect_one();
@@ -1003,13 +1017,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP, kFolds<O
     }
   } else {
     // ---------------------------------------------------------- epilogue (both CTAs)
-    if constexpr (kFold) regs_up<kRegsHigh>();
+    regs_up<kRegsHigh>();
     const int sub = warp & 3;                    // TMEM lane quadrant
     const int m_local = sub * 32 + lane;
-    const int from = kFold ? ((warp - C::kEpi0) >> 2) * 128 : 0;   // kFold: the warp's 128 columns
+    const int from = ((warp - C::kEpi0) >> 2) * 128;             // the warp's 128 columns
     uint8_t* stg = staging + (warp - C::kEpi0) * C::kWarpStage;
     EpilogueSync sync{epi_bar, abort_flag, status};
-    uint32_t it = 0, stores = 0;
+    uint32_t it = 0;
     bool ok = true;
     auto release = [&](uint32_t b) {
       tc_fence_before();
@@ -1019,7 +1033,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP, kFolds<O
     while (ok && fetch()) {
       const int m0 = t.mb * 256 + rank * 128 + sub * 32;          // the warp's first output index
       const int cols = OP == kTN ? grad_cols() : t.rows;          // TMEM columns in use
-      const int to = kFold ? min(cols, from + 128) : cols;
+      const int to = min(cols, from + 128);
       int first = 0, last = 0;
       if (cut) sched.owners(c.tile, first, last);
       auto slot = [&](int owner) {
@@ -1049,8 +1063,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP, kFolds<O
       // lies past n and k
       constexpr int kStep = 128 / static_cast<int>(sizeof(OUT));
       auto box_out = [&](const float* v, int n0) {
-        uint8_t* box = stg + stores % C::kBoxes * 4096;
-        if (lane == 0) bulk_wait_read<C::kBoxes - 1>();           // an earlier store has left this stage
+        if (lane == 0) bulk_wait_read<0>();                       // the store before has left the stage
         __syncwarp();
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -1063,96 +1076,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP, kFolds<O
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = __floats2bfloat162_rn(v[8 * u + 2 * e], v[8 * u + 2 * e + 1]);
           }
-          *reinterpret_cast<uint4*>(box + lane * 128 + ((u ^ (lane & 7)) << 4)) = q;
+          *reinterpret_cast<uint4*>(stg + lane * 128 + ((u ^ (lane & 7)) << 4)) = q;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (m0 < p.m_total) tma_store_3d(&p.omap, box, t.nb * 256 + n0, m0, t.g);
+          if (m0 < p.m_total) tma_store_3d(&p.omap, stg, t.nb * 256 + n0, m0, t.g);
           bulk_commit();
         }
-        ++stores;
       };
       const uint32_t lanes = tmem + (static_cast<uint32_t>(sub * 32) << 16);
-      if constexpr (kFold) {
-        f32x2 acc[64];                           // the warp's 128 columns
+      f32x2 acc[64];                             // the warp's 128 columns (TN: zeros for no rows)
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = both2(0.f);
-        for (int kb = c.kb0; kb < c.kb1; kb += kRun, ++it) {
-          const uint32_t b = it % C::kBufs;
-          ok = mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
-          if (!ok) break;
-          tc_fence_after();
-          if (from < to) {
-            const uint32_t tb = lanes + b * C::kCols + from;
-            uint32_t v[2][16];
-            tmem_ld16_begin(tb, v[0]);
-            tmem_ld_end(v[0]);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              if (q < 7) tmem_ld16_begin(tb + (q + 1) * 16, v[(q + 1) & 1]);
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) {
-                f32x2& a = acc[(q * 16 + i) / 2];
-                a = add2(a, pack2(v[q & 1][i], v[q & 1][i + 1]));
-              }
-              if (q < 7) tmem_ld_end(v[(q + 1) & 1]);
-            }
-          }
-          release(b);
-        }
+      for (int i = 0; i < 64; ++i) acc[i] = both2(0.f);
+      for (int kb = c.kb0; kb < c.kb1; kb += kRun, ++it) {
+        const uint32_t b = it % C::kBufs;
+        ok = mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status);
         if (!ok) break;
-        auto sums = [&](int i, float* v, auto n) {
+        tc_fence_after();
+        const uint32_t tb = lanes + b * C::kCols + from;
+        if (from < to) add_columns(tb, to - from, acc);
+        release(b);
+      }
+      if (!ok) break;
+      auto sums = [&](int i, float* v, auto n) {
 #pragma unroll
-          for (int e = 0; e < decltype(n)::value / 2; ++e) {
-            const float2 f = unpack2(acc[i / 2 + e]);
-            v[2 * e] = f.x;
-            v[2 * e + 1] = f.y;
-          }
-        };
-        if (OP == kTN && !cut) {
+        for (int e = 0; e < decltype(n)::value / 2; ++e) {
+          const float2 f = unpack2(acc[i / 2 + e]);
+          v[2 * e] = f.x;
+          v[2 * e + 1] = f.y;
+        }
+      };
+      if (OP == kTN && !cut) {
 #pragma unroll
-          for (int i = 0; i < 128; i += 32) {
-            float v[32];
-            sums(i, v, std::integral_constant<int, 32>());
-            if (from + i < to) box_out(v, from + i);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 128; i += 16) {
-            float v[16];
-            sums(i, v, std::integral_constant<int, 16>());
-            if (from + i < to) emit(v, from + i);
-          }
+        for (int i = 0; i < 128; i += kStep) {
+          float v[kStep];
+          sums(i, v, std::integral_constant<int, kStep>());
+          if (from + i < to) box_out(v, from + i);
         }
       } else {
-        const bool rows = c.kb1 > c.kb0;         // false (TN): a group without rows, zeros
-        const uint32_t b = it % C::kBufs, tb = lanes + b * C::kCols;
-        if (rows) {
-          if (!mbar_wait_warp(&tfull_bar[b], (it / C::kBufs) & 1u, abort_flag, status)) break;
-          tc_fence_after();
-        }
-        if (OP == kTN && !cut) {
-          for (int n0 = 0; n0 < cols; n0 += 64) {
-            float v[64];
-            if (rows) {
-              tmem_ld64(tb + n0, v);
-            } else {
 #pragma unroll
-              for (int i = 0; i < 64; ++i) v[i] = 0.f;
-            }
-            box_out(v, n0);
-          }
-        } else {
-          for (int n0 = 0; n0 < cols; n0 += 16) {
-            float v[16];
-            tmem_ld16(tb + n0, v);
-            emit(v, n0);
-          }
-        }
-        if (rows) {
-          release(b);
-          ++it;
+        for (int i = 0; i < 128; i += 16) {
+          float v[16];
+          sums(i, v, std::integral_constant<int, 16>());
+          if (from + i < to) emit(v, from + i);
         }
       }
       if (!cut) continue;
@@ -1520,7 +1487,7 @@ cudaError_t launch_product_kernel(K kernel, const ProductArgs& a, int grid, int 
 
 template <bool F8, int OP, typename OUT>
 cudaError_t launch_product(const ProductArgs& a, bool stream_tiles, cudaStream_t s) {
-  using Pair = PairCfg<OP, kFolds<OUT>>;
+  using Pair = PairCfg<OP>;
   const int sms = device_sms();
   if (sms < 2) return cudaErrorInvalidDevice;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
