@@ -49,8 +49,12 @@ constexpr int kMaxCounters = 192;
 // bf16 operands: K blocks that the tensor cores sum before the sum is added to fp32 registers.  They
 // cut each addend at 2^-23 of the largest, which leaves a sum about 1.1e-9 of its value short per
 // element (7.9e-6 at 7168, which moves one bf16 rounding in 500); sums of 512 elements are short by
-// 6e-7, and adding them in fp32 rounds once each.
-constexpr int kFoldBlocks = 8;
+// 6e-7.  Adding m of them one after another in fp32 would round m times, the same way each time where
+// the addends are alike: 2.4e-4 of a weight gradient over 2^23 rows.  kFoldSums of them are therefore
+// added to one, and those to one another, at most (kFoldSums + m / kFoldSums) / 2^24 of the magnitudes.
+// (TN, whose inner index are rows; the other products add 128 sums at most.)
+constexpr int kFoldBlocks = 8, kFoldSums = 64;
+constexpr int kLevel = kFoldBlocks * kFoldSums; // K blocks of such a sum
 // Eight epilogue warps that keep 128 sums and 32 products per thread (pair and fold kernel):
 // registers move from warps 0..3 to 4..11, 384 x 168 at launch = 128 x 40 + 256 x 232.
 constexpr int kRegsLow = 40, kRegsHigh = 232;
@@ -446,6 +450,29 @@ __device__ __forceinline__ void add_columns(uint32_t tb, int cols, f32x2 (&acc)[
   }
 }
 
+// The warp's first `cols` of 128 columns, for the level above of a very long sum: acc is put (first) or
+// added to a thread's place in the workspace and is zero afterwards, or takes what is there.
+__device__ __forceinline__ void lay_aside(float* place, int cols, bool first, f32x2 (&acc)[64]) {
+#pragma unroll
+  for (int i = 0; i < 128; i += 4) {
+    if (i >= cols) break;
+    float4* at = reinterpret_cast<float4*>(place + i * 128);
+    const float4 x = first ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldcg(at);
+    const float2 a = unpack2(acc[i / 2]), b = unpack2(acc[i / 2 + 1]);
+    __stcg(at, make_float4(x.x + a.x, x.y + a.y, x.z + b.x, x.w + b.y));
+    acc[i / 2] = acc[i / 2 + 1] = both2(0.f);
+  }
+}
+__device__ __forceinline__ void take_back(const float* place, int cols, f32x2 (&acc)[64]) {
+#pragma unroll
+  for (int i = 0; i < 128; i += 4) {
+    if (i >= cols) break;
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(place + i * 128));
+    acc[i / 2] = add2(acc[i / 2], pack2(x.x, x.y));
+    acc[i / 2 + 1] = add2(acc[i / 2 + 1], pack2(x.z, x.w));
+  }
+}
+
 // ------------------------------------------------------------------ stream kernel
 // Groups of few rows: every weight byte is used for a handful of tokens, so HBM bounds it and the
 // tile is made for a steady stream.  The weights are the M side (256 rows per tile, two MMAs), the
@@ -796,7 +823,8 @@ __device__ __forceinline__ bool ragged_block(int rows, int kb) {
   return left < 64 && (left & 15) != 0;
 }
 
-template <int OP, typename OUT>
+// LONG (TN): sums of more than kFoldSums partial sums.
+template <int OP, typename OUT, bool LONG>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThreads, 1)
     pair_kernel(const __grid_constant__ ProductArgs p) {
   constexpr int kRun = kFoldBlocks;              // K blocks per accumulator
@@ -1097,8 +1125,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
         const uint32_t tb = lanes + b * C::kCols + from;
         if (from < to) add_columns(tb, to - from, acc);
         release(b);
+        const int done = kb + kRun - c.kb0;
+        if (LONG && done % kLevel == 0 && done < c.kb1 - c.kb0)
+          // (this pair's part of the workspace: its cut tile, if any, comes last and ends there too)
+          lay_aside(slot(pair) + from * 128, to - from, done == kLevel, acc);
       }
       if (!ok) break;
+      if (LONG && c.kb1 - c.kb0 > kLevel) take_back(slot(pair) + from * 128, to - from, acc);
       auto sums = [&](int i, float* v, auto n) {
 #pragma unroll
         for (int e = 0; e < decltype(n)::value / 2; ++e) {
@@ -1495,8 +1528,16 @@ cudaError_t launch_product(const ProductArgs& a, bool stream_tiles, cudaStream_t
     if (stream_tiles)
       return launch_product_kernel(stream_kernel<F8, OP, OUT>, a, ctas, 224, StreamCfg<F8, OP>::kSmem, s);
   }
-  if constexpr (F8) return launch_product_kernel(fold_kernel<OUT>, a, ctas, FoldCfg::kThreads, FoldCfg::kSmem, s);
-  else return launch_product_kernel(pair_kernel<OP, OUT>, a, ctas / 2 * 2, Pair::kThreads, Pair::kSmem, s);
+  if constexpr (F8) {
+    return launch_product_kernel(fold_kernel<OUT>, a, ctas, FoldCfg::kThreads, FoldCfg::kSmem, s);
+  } else {
+    // a second level of sums only where a group can have the rows for it: the code for it costs
+    // registers (weight gradient of 32 groups x 256 rows: 459 us without, 468 with)
+    auto kernel = pair_kernel<OP, OUT, false>;
+    if constexpr (OP == kTN)
+      if (a.n_rows > 64 * kLevel) kernel = pair_kernel<OP, OUT, true>;
+    return launch_product_kernel(kernel, a, ctas / 2 * 2, Pair::kThreads, Pair::kSmem, s);
+  }
 }
 template <bool F8, int OP>
 moe_status launch_product(const ProductArgs& a, bool f32, bool stream_tiles, cudaStream_t s) {

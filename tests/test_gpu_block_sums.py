@@ -50,3 +50,52 @@ def test_bf16_outputs_are_roundings_of_32_bit_sums(op, rows, n, k):
     rounded = ref.to(BF).double()
     off = float((got.double() - rounded).norm() / rounded.norm())
     assert off <= (50 * 2.0 ** -24 * 2.0 ** -7) ** 0.5, off
+
+
+@pytest.mark.parametrize("groups,rows", [(2, 1 << 20), (2, 1 << 23), (1, 1 << 24)])
+def test_sums_over_millions_of_rows(groups, rows):
+    """A weight gradient over so many rows that adding sums of 512 one after another would round the
+    same way thousands of times.  dy is 1, and each 512 rows of a add up to 512 + j / 128 exactly (j
+    per column), which every binade of a running sum cuts off elsewhere.  Of m sums of 512, 64 are
+    added to one, and those m / 64 to the next, with one rounding of half a step each; up to 4 parts
+    of a cut tile and the output round once more: 64 + m / 64 + 5 times 2^-24 of the value."""
+    total = groups * rows
+    a = torch.ones(total, 8, device=DEV, dtype=BF)
+    extra = (4 * torch.arange(8, device=DEV) + 3).to(BF) / 128
+    a.view(-1, 512, 8)[:, 5] += extra
+    dy = torch.ones(total, 8, device=DEV, dtype=BF)
+    cfg = moe.make_product_config(groups, total, 8, 8, out="f32")
+    off = (rows * torch.arange(groups + 1, device=DEV)).to(torch.int32)
+    ws, dw = product_ws(cfg), torch.empty(groups, 8, 8, device=DEV)
+    moe.moe_grouped_gemm_wgrad(cfg, off, dy, a, dw, ws)
+    assert moe.moe_read_device_status(ws) == 0 and (ws[:256] == 0).all()
+    m = rows // 512
+    want = m * (512 + extra.double())
+    off = float(((dw.double() - want).abs() / want).max())
+    assert off <= (64 + m / 64 + 5) * 2.0 ** -24, off
+
+
+@pytest.mark.parametrize("out", [BF, torch.float32])
+def test_long_ragged_weight_gradients(out):
+    """Groups of odd sizes on both sides of the second level of sums, columns behind a tile's last.  In
+    32 bits the root mean square of the errors is below that of one sum of 512 (32 steps of the tensor
+    cores, 2^-24 each) and of the roundings of 64 + 3 additions and 5 of parts and output, 104 * 2^-24
+    of the results' (running sums are smaller than their results)."""
+    sizes, n, k = [70001, 0, 5, 32768, 32769, 40003], 264, 200
+    g = torch.Generator(DEV).manual_seed(9)
+    R = sum(sizes) + 7
+    dy, a = (torch.randn(R, c, device=DEV, generator=g).to(BF) for c in (n, k))
+    dy[sum(sizes):] = float("nan")
+    off = torch.tensor([0] + sizes, device=DEV).cumsum(0).to(torch.int32)
+    cfg = moe.make_product_config(len(sizes), R, n, k, out="bf16" if out == BF else "f32")
+    ws, dw = product_ws(cfg), torch.full((len(sizes), n, k), float("nan"), device=DEV, dtype=out)
+    moe.moe_grouped_gemm_wgrad(cfg, off, dy, a, dw, ws)
+    assert moe.moe_read_device_status(ws) == 0 and (ws[:256] == 0).all()
+    bar = 104 * 2.0 ** -24
+    for i, m in enumerate(sizes):
+        lo = sum(sizes[:i])
+        ref = dy[lo:lo + m].double().T @ a[lo:lo + m].double()
+        if out == BF:                            # see test_bf16_outputs_are_roundings_of_32_bit_sums
+            ref = ref.to(BF).double()
+        error = (dw[i].double() - ref).square().mean().sqrt()
+        assert error <= (bar if out != BF else (bar * 2.0 ** -7) ** 0.5) * ref.square().mean().sqrt(), (m, float(error))
