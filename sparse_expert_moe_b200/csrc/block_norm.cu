@@ -846,7 +846,8 @@ moe_status moe_block_norm_backward(const moe_norm_config* cfg, const void* r_out
                                    cudaStream_t stream) {
   const moe_status st = check_norm(cfg);
   if (st != MOE_OK) return st;
-  if (!ws || (dgate && cfg->gate == MOE_GATE_NONE) || (dw_post && !w_post) || (dw_pre && !w_pre))
+  if (!ws || (dgate && cfg->gate == MOE_GATE_NONE) || (dw_post && !w_post) || (dw_pre && !w_pre) ||
+      (cfg->gate == MOE_GATE_CHANNEL && !gate))
     return MOE_ERR_INVALID_ARG;
   if (cfg->T > 0 &&                              // (tensors of no rows have no address to check)
       ((cfg->gate != MOE_GATE_NONE) != (gate != nullptr) || (!y && (w_post || gate)) || !w_pre != !dh || !y != !dy ||
@@ -857,6 +858,13 @@ moe_status moe_block_norm_backward(const moe_norm_config* cfg, const void* r_out
       unaligned16(dw_pre) || (cfg->gate != MOE_GATE_TOKEN && (unaligned16(gate) || unaligned16(dgate))))
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < backward_workspace(*cfg)) return MOE_ERR_WORKSPACE;
+  if (cfg->T == 0) {                             // empty sums, whatever gate and weights hold
+    const size_t bytes = sizeof(float) * cfg->d_model;
+    for (void* sum : {static_cast<void*>(dw_pre), static_cast<void*>(dw_post),
+                      cfg->gate == MOE_GATE_CHANNEL ? dgate : nullptr})
+      if (sum && cudaMemsetAsync(sum, 0, bytes, stream) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
   const BackwardShape sh = backward_shape(cfg->d_model);
   const int64_t turns = (static_cast<int64_t>(cfg->T) + sh.rows - 1) / sh.rows;
   const unsigned grid = static_cast<unsigned>(turns < kBackwardCtas ? turns : kBackwardCtas);
@@ -879,16 +887,13 @@ moe_status moe_block_norm_backward(const moe_norm_config* cfg, const void* r_out
   a.branch_scale = cfg->branch_scale;
   a.w_offset = cfg->w_offset;
   const bool res32 = cfg->res == MOE_F32, act32 = cfg->act == MOE_F32;
-  if (grid) {
-    const cudaError_t e = sh.vpt == 1 ? launch_backward<1>(a, res32, act32, grid, stream)
-                                      : (sh.vpt == 2 ? launch_backward<2>(a, res32, act32, grid, stream)
-                                                     : launch_backward<4>(a, res32, act32, grid, stream));
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
-  }
+  const cudaError_t e = sh.vpt == 1 ? launch_backward<1>(a, res32, act32, grid, stream)
+                                    : (sh.vpt == 2 ? launch_backward<2>(a, res32, act32, grid, stream)
+                                                   : launch_backward<4>(a, res32, act32, grid, stream));
+  if (e != cudaSuccess) return MOE_ERR_CUDA;
   float* dgc = cfg->gate == MOE_GATE_CHANNEL ? static_cast<float*>(dgate) : nullptr;
-  if (a.want_pre || a.want_branch) {
+  if (a.want_pre || a.want_branch)
     return ok_or_cuda(launch_overlapped(sum_parts_kernel, dim3((a.d + 31) / 32, 2), 256, 0, stream, a, dw_pre, dw_post, dgc));
-  }
   return MOE_OK;
 }
 

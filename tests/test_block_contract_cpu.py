@@ -1,0 +1,43 @@
+"""Calls of the block norms and the grouped products that have to be refused on the host, without a
+GPU (`FAKE` is an aligned address that none of these paths dereferences)."""
+import ctypes
+import os
+
+import pytest
+
+from sparse_expert_moe_b200 import moe
+
+FAKE = 256
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(moe.LIB_PATH):
+        from sparse_expert_moe_b200 import build
+        build.build()
+    return moe.load_library()
+
+
+BWD = ("r_out", "y", "w_post", "gate", "w_pre", "dh", "dr_out", "dr", "dy", "dgate", "dw_post", "dw_pre")
+
+
+def backward_code(lib, config, **kw):
+    a = {k: FAKE for k in BWD}
+    a.update(kw)
+    return lib.moe_block_norm_backward(ctypes.byref(config), *[a[k] for k in BWD], FAKE, 1 << 30, None)
+
+
+@pytest.mark.parametrize("T", [0, 4])
+def test_a_channel_gate_is_needed_without_rows_too(lib, T):
+    """A [d] operand exists at every T; what has no rows may have no address."""
+    c = moe.make_norm_config(T, 256, gate="channel")
+    assert backward_code(lib, c, gate=None) == 1
+    assert backward_code(lib, c, gate=None, dgate=None, dw_post=None, dw_pre=None) == 1
+
+
+@pytest.mark.parametrize("gate", ["none", "token", "full"])
+def test_backward_of_no_rows_has_no_addresses(lib, gate):
+    """Nothing to compute, nothing to write: no launch, so the answer comes without a GPU."""
+    c = moe.make_norm_config(0, 256, gate=gate)
+    none = dict.fromkeys(("r_out", "y", "gate", "dh", "dr_out", "dr", "dy", "dgate", "dw_post", "dw_pre"))
+    assert backward_code(lib, c, **none) == 0
