@@ -78,7 +78,9 @@ typedef enum {
   MOE_ERR_TIMEOUT = 6,        /* device status: a bounded in-kernel wait ran out */
   MOE_ERR_DEVICE_VALUE = 7    /* device status: an FP8 block scale that is not a positive,
                                  normal power of two (the tensor cores take the scale's
-                                 exponent only); the results of that call are not valid */
+                                 exponent only), or (moe_grouped_gemm) two fp32 scales
+                                 whose product overflows; the results of that call are not
+                                 valid */
 } moe_status;
 
 /* Router score function.
@@ -383,8 +385,11 @@ MOE_API moe_status moe_product_workspace_size(const moe_product_config *cfg, siz
  *   a_scale, w_scale  MOE_E4M3_FP32_SCALE: fp32 [n_rows, ceil(k/128)] and
  *                 [n_groups, ceil(n/128), ceil(k/128)], one scale per 128 codes of a row and per
  *                 128 x 128 codes of a weight, of any finite value; else NULL.  The product of
- *                 each 128-k block is summed on the tensor cores and multiplied by its two
- *                 scales in fp32.
+ *                 each 128-k block is summed on the tensor cores and multiplied by the product
+ *                 of its two scales in fp32.  Where that overflows, the device status becomes
+ *                 MOE_ERR_DEVICE_VALUE and the outputs concerned are infinite or NaN; where it
+ *                 is below 2^-126 it rounds as a subnormal number, which moves the block's
+ *                 share by 2^-125 at most.
  * A dense 8-bit product is this call with one group.  a, w, y 16-byte aligned.  The first 256
  * bytes of the workspace hold the device status (moe_reset_device_status once before use). */
 MOE_API moe_status moe_grouped_gemm(const moe_product_config *cfg, const int32_t *group_offsets,

@@ -1021,7 +1021,7 @@ const char* moe_status_string(moe_status s) {
     case MOE_ERR_CUDA: return "CUDA error";
     case MOE_ERR_DEVICE_INDEX: return "device: index or offset out of range";
     case MOE_ERR_TIMEOUT: return "device: bounded wait timed out";
-    case MOE_ERR_DEVICE_VALUE: return "device: FP8 block scale not a positive normal power of two";
+    case MOE_ERR_DEVICE_VALUE: return "device: FP8 block scale not a positive normal power of two, or two whose product overflows";
   }
   return "unknown status";
 }
