@@ -5,9 +5,9 @@
 //   r' = a r + b g u
 //   h = r' i_r (w_pre + o),  i_r = (mean r'^2 + eps)^-1/2
 // and backwards, with z = dh (w_pre + o) and G the whole gradient of r':
-//   G  = dr' + i_r z - r' i_r^3 mean(z r')          dr = a G       dw_pre  = sum_t dh r' i_r
+//   G  = dr' + i_r (z - r' i_r (i_r mean(z r')))    dr = a G       dw_pre  = sum_t dh r' i_r
 //   q  = b g G (w_post + o)                                        dw_post = sum_t b g G y i_y
-//   dy = i_y q - y i_y^3 mean(q y)                                 dgate   = sum b G u
+//   dy = i_y (q - y i_y (i_y mean(q y)))                           dgate   = sum b G u
 // All arithmetic is fp32; each output is rounded once.  The backward pass recomputes both
 // statistics from the rows it reads anyway, so the forward pass stores none.
 //
@@ -509,7 +509,9 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
     m[0] = m[1] = 0.f;
     if (t >= p.T) return;
     const size_t base = static_cast<size_t>(t) * p.nvec;
-    const f32x2 k_r = both2(-i_r * i_r * i_r * (zr * p.inv_d));
+    // x^ = r' i_r stands for r' throughout: i_r^3 by itself leaves the range of fp32 (rows of zeros
+    // with an eps below 1e-25, rows past 1e12)
+    const f32x2 k_r = both2(-i_r * (zr * p.inv_d));
     f32x2 m0 = both2(0.f), m1 = both2(0.f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -524,10 +526,10 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
         Vec8 zx;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const f32x2 zi = mul2(z.p[e], both2(i_r));
-          if (!kSmem) A[kSmem ? 0 : j].p[e] = fma2(zi, x.p[e], A[kSmem ? 0 : j].p[e]);
-          else zx.p[e] = mul2(zi, x.p[e]);
-          G.p[e] = fma2(zi, wj.p[e], fma2(k_r, x.p[e], G.p[e]));
+          const f32x2 n = mul2(x.p[e], both2(i_r));
+          if (!kSmem) A[kSmem ? 0 : j].p[e] = fma2(z.p[e], n, A[kSmem ? 0 : j].p[e]);
+          else zx.p[e] = mul2(z.p[e], n);
+          G.p[e] = fma2(both2(i_r), fma2(z.p[e], wj.p[e], mul2(k_r, n)), G.p[e]);
         }
         if (kSmem && p.want_pre) smem_add(0, v, zx);
       }
@@ -574,7 +576,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
   auto branch_gradient = [&](int t, const uint4* st, float i_y, float qy, float gu) {
     if (t >= p.T || !branch) return;
     const size_t base = static_cast<size_t>(t) * p.nvec;
-    const f32x2 k_y = both2(-i_y * i_y * i_y * (qy * p.inv_d));
+    const f32x2 k_y = both2(-i_y * (qy * p.inv_d));
     if (i0 == 0 && p.want_gate && p.gate_kind == MOE_GATE_TOKEN) static_cast<float*>(p.dgate)[t] = gu;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -583,7 +585,8 @@ __global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGrad
       if (post) {
         const Vec8 y = row8<ACT32, kPitch>(st + kAtY * kPitch, j, p.y, base + v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) q[j].p[e] = fma2(both2(i_y), q[j].p[e], mul2(k_y, y.p[e]));
+        for (int e = 0; e < 4; ++e)
+          q[j].p[e] = mul2(both2(i_y), fma2(k_y, mul2(y.p[e], both2(i_y)), q[j].p[e]));
       }
       store8(p.dy, base + v, ACT32, q[j]);
     }
