@@ -390,7 +390,8 @@ MOE_API moe_status moe_product_workspace_size(const moe_product_config *cfg, siz
  *                 MOE_ERR_DEVICE_VALUE and the outputs concerned are infinite or NaN; where it
  *                 is below 2^-126 it rounds as a subnormal number, which moves the block's
  *                 share by 2^-125 at most.
- * A dense 8-bit product is this call with one group.  a, w, y 16-byte aligned.  The first 256
+ * A dense 8-bit product is this call with one group.  a, w, y 16-byte aligned, scales and
+ * group_offsets by their elements.  The first 256
  * bytes of the workspace hold the device status (moe_reset_device_status once before use). */
 MOE_API moe_status moe_grouped_gemm(const moe_product_config *cfg, const int32_t *group_offsets,
                                     const void *a, const float *a_scale, const void *w,

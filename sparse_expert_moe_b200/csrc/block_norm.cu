@@ -717,7 +717,10 @@ size_t backward_workspace(const moe_norm_config& c) {
   return kNormHeader + sizeof(float) * 2 * static_cast<size_t>(kBackwardCtas) * s.rows * c.d_model;
 }
 
-bool unaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+// A token gate is read by the element.
+size_t gate_alignment(const moe_norm_config& c) {
+  return c.gate != MOE_GATE_TOKEN ? 16 : (c.weight == MOE_F32 ? 4 : 2);
+}
 
 moe_status ok_or_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
@@ -816,8 +819,8 @@ moe_status moe_block_norm(const moe_norm_config* cfg, const void* r, const void*
   if ((cfg->gate != MOE_GATE_NONE) != (gate != nullptr) || (!y && (w_post || gate)) || !w_pre != !h ||
       (h && (cfg->out == MOE_E4M3) != (h_scale != nullptr)) || (!h && h_scale) || (!r_out && !h) || !r)
     return MOE_ERR_INVALID_ARG;
-  if (unaligned16(r) || unaligned16(y) || unaligned16(w_post) || unaligned16(w_pre) || unaligned16(r_out) ||
-      unaligned16(h) || (cfg->gate != MOE_GATE_TOKEN && unaligned16(gate)))
+  if (misaligned(r) || misaligned(y) || misaligned(w_post) || misaligned(w_pre) || misaligned(r_out) ||
+      misaligned(h) || misaligned(gate, gate_alignment(*cfg)) || misaligned(h_scale, sizeof(float)))
     return MOE_ERR_INVALID_ARG;
   NormArgs a{r, y, w_post, gate, w_pre, r_out, h, h_scale};
   a.T = cfg->T;
@@ -856,9 +859,10 @@ moe_status moe_block_norm_backward(const moe_norm_config* cfg, const void* r_out
       ((cfg->gate != MOE_GATE_NONE) != (gate != nullptr) || (!y && (w_post || gate)) || !w_pre != !dh || !y != !dy ||
        !dr || (w_pre && !r_out) || (!dh && !dr_out)))
     return MOE_ERR_INVALID_ARG;
-  if (unaligned16(r_out) || unaligned16(y) || unaligned16(w_post) || unaligned16(w_pre) || unaligned16(dh) ||
-      unaligned16(dr_out) || unaligned16(dr) || unaligned16(dy) || unaligned16(ws) || unaligned16(dw_post) ||
-      unaligned16(dw_pre) || (cfg->gate != MOE_GATE_TOKEN && (unaligned16(gate) || unaligned16(dgate))))
+  if (misaligned(r_out) || misaligned(y) || misaligned(w_post) || misaligned(w_pre) || misaligned(dh) ||
+      misaligned(dr_out) || misaligned(dr) || misaligned(dy) || misaligned(ws) || misaligned(dw_post) ||
+      misaligned(dw_pre) || misaligned(gate, gate_alignment(*cfg)) ||
+      misaligned(dgate, cfg->gate == MOE_GATE_TOKEN ? sizeof(float) : 16))
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < backward_workspace(*cfg)) return MOE_ERR_WORKSPACE;
   if (cfg->T == 0) {                             // empty sums, whatever gate and weights hold

@@ -1527,8 +1527,6 @@ int device_sms() {
   return n;
 }
 
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
 moe_status check_product(const moe_product_config* c) {
   if (!c || c->n_groups <= 0 || c->n_rows < 0 || c->n <= 0 || c->k <= 0) return MOE_ERR_INVALID_ARG;
   if (c->n_groups > kMaxProductGroups || c->n > 65536 || c->k > 65536 || c->n_rows > (1 << 24))
@@ -1591,7 +1589,8 @@ moe_status common_checks(const moe_product_config* cfg, const int32_t* offsets, 
   const moe_status st = check_product(cfg);
   if (st != MOE_OK) return st;
   if (!ws || (!offsets && cfg->n_groups != 1)) return MOE_ERR_INVALID_ARG;
-  if (misaligned(x) || misaligned(y) || misaligned(z) || misaligned(ws)) return MOE_ERR_INVALID_ARG;
+  if (misaligned(x) || misaligned(y) || misaligned(z) || misaligned(ws) || misaligned(offsets, sizeof(int32_t)))
+    return MOE_ERR_INVALID_ARG;
   return ws_bytes < product_workspace() ? MOE_ERR_WORKSPACE : MOE_OK;
 }
 
@@ -1628,6 +1627,7 @@ moe_status moe_grouped_gemm(const moe_product_config* cfg, const int32_t* group_
   if (st != MOE_OK) return st;
   const bool f8 = cfg->in == MOE_E4M3_FP32_SCALE;
   if (!f8 && (a_scale || w_scale)) return MOE_ERR_INVALID_ARG;
+  if (misaligned(a_scale, sizeof(float)) || misaligned(w_scale, sizeof(float))) return MOE_ERR_INVALID_ARG;
   if (cfg->n_rows == 0) return MOE_OK;
   if (!a || !w || !y || (f8 && (!a_scale || !w_scale))) return MOE_ERR_INVALID_ARG;
   ProductArgs p = product_args(*cfg, group_offsets, y, ws);

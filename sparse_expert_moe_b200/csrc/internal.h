@@ -26,6 +26,11 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
   return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
 }
 
+// An address that is not a multiple of `bytes`, a power of two.
+inline bool misaligned(const void* p, size_t bytes = 16) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
+}
+
 // Host-side configuration checks shared by every entry point (MOE_OK or the error code).
 moe_status validate_config(const moe_config* c);
 

@@ -41,3 +41,29 @@ def test_backward_of_no_rows_has_no_addresses(lib, gate):
     c = moe.make_norm_config(0, 256, gate=gate)
     none = dict.fromkeys(("r_out", "y", "gate", "dh", "dr_out", "dr", "dy", "dgate", "dw_post", "dw_pre"))
     assert backward_code(lib, c, **none) == 0
+
+
+def norm_code(lib, config, gate=None, h_scale=None):
+    return lib.moe_block_norm(ctypes.byref(config), FAKE, FAKE, FAKE, gate, FAKE, FAKE, FAKE, h_scale, None)
+
+
+@pytest.mark.parametrize("weight,gate", [("bf16", FAKE + 1), ("f32", FAKE + 1), ("f32", FAKE + 2)])
+def test_token_gates_have_their_elements_alignment(lib, weight, gate):
+    c = moe.make_norm_config(4, 256, gate="token", weight=weight)
+    assert norm_code(lib, c, gate=gate) == 1
+    assert backward_code(lib, c, gate=gate) == 1
+    assert backward_code(lib, c, dgate=FAKE + 2) == 1
+
+
+def test_scales_and_offsets_have_their_elements_alignment(lib):
+    for odd in (1, 2):
+        assert norm_code(lib, moe.make_norm_config(4, 256, out="e4m3"), h_scale=FAKE + odd) == 1
+    c, f8 = (moe.make_product_config(4, 10, 256, 128, dtype=t) for t in ("bf16", "e4m3_fs"))
+    size = moe.moe_product_workspace_size(c)
+
+    def gemm(config, off=FAKE, sa=None, sw=None):
+        return lib.moe_grouped_gemm(ctypes.byref(config), off, FAKE, sa, FAKE, sw, FAKE, FAKE, size, None)
+    assert gemm(c, off=FAKE + 2) == 1
+    assert gemm(f8, sa=FAKE + 2, sw=FAKE) == 1 and gemm(f8, sa=FAKE, sw=FAKE + 1) == 1
+    for fn in (lib.moe_grouped_gemm_dgrad, lib.moe_grouped_gemm_wgrad):
+        assert fn(ctypes.byref(c), FAKE + 2, FAKE, FAKE, FAKE, FAKE, size, None) == 1
