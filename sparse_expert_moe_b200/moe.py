@@ -284,21 +284,36 @@ def _device_of(*tensors) -> int:
     return -1
 
 
-def _addr(fn: str, name: str, t, want, numel: int, device: int):
+def _in_rows(t, row: int) -> bool:
+    """Whether a tensor's last dimensions are `row` elements together, or it is flat."""
+    if t.dim() < 2:
+        return True
+    n = 1
+    for size in reversed(t.shape):
+        if n == row:
+            return True
+        n *= size
+    return n == row or n == 0                    # one row, or no elements
+
+
+def _addr(fn: str, name: str, t, want, numel: int, device: int, row: int = 0):
     """Device address of a tensor of one call, checked: its type (None: any), element count,
-    contiguity and device.  None and plain integers (device addresses) pass."""
+    contiguity and device, and (matrices of a product) the length of its rows, which is what tells a
+    weight from its transpose.  None and plain integers (device addresses) pass."""
     if t is None or type(t) is int:
         return t
     if (t.dtype is want or want is None) and t.numel() == numel and t.is_contiguous() and \
-            t.get_device() == device:
+            t.get_device() == device and (not row or t.shape[-1] == row or _in_rows(t, row)):
         return t.data_ptr()
     if want is torch.float8_e4m3fn and t.dtype is torch.uint8:       # codes as bytes
-        return _addr(fn, name, t, torch.uint8, numel, device)
+        return _addr(fn, name, t, torch.uint8, numel, device, row)
     if want is not None and t.dtype is not want:
         raise TypeError(f"{fn}: {name} is {t.dtype}, not {want}")
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be contiguous with {numel} elements, got shape "
                          f"{tuple(t.shape)}, strides {t.stride()}")
+    if row and not _in_rows(t, row):
+        raise ValueError(f"{fn}: {name} must have rows of {row} elements, got shape {tuple(t.shape)}")
     raise ValueError(f"{fn}: {name} is not on the CUDA device of the other tensors")
 
 
@@ -393,10 +408,10 @@ def moe_grouped_gemm(cfg: MoeProductConfig, group_offsets, a, a_scale, w, w_scal
     G, R, n, k, vt = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k, _VALUE_TYPES.get(cfg.in_)
     kb = (k + 127) // 128
     _call(fn, dev, stream, ctypes.byref(cfg),
-          _addr(fn, "group_offsets", group_offsets, torch.int32, G + 1, dev), _addr(fn, "a", a, vt, R * k, dev),
-          _addr(fn, "a_scale", a_scale, f32, R * kb, dev), _addr(fn, "w", w, vt, G * n * k, dev),
-          _addr(fn, "w_scale", w_scale, f32, G * ((n + 127) // 128) * kb, dev),
-          _addr(fn, "y", y, _VALUE_TYPES.get(cfg.out), R * n, dev), *_workspace(fn, ws, dev))
+          _addr(fn, "group_offsets", group_offsets, torch.int32, G + 1, dev), _addr(fn, "a", a, vt, R * k, dev, k),
+          _addr(fn, "a_scale", a_scale, f32, R * kb, dev, kb), _addr(fn, "w", w, vt, G * n * k, dev, k),
+          _addr(fn, "w_scale", w_scale, f32, G * ((n + 127) // 128) * kb, dev, kb),
+          _addr(fn, "y", y, _VALUE_TYPES.get(cfg.out), R * n, dev, n), *_workspace(fn, ws, dev))
 
 
 def moe_grouped_gemm_dgrad(cfg: MoeProductConfig, group_offsets, dy, w, da, ws, stream=None):
@@ -405,8 +420,8 @@ def moe_grouped_gemm_dgrad(cfg: MoeProductConfig, group_offsets, dy, w, da, ws, 
     dev = _device_of(dy, w, da, group_offsets, ws)
     G, R, n, k, vt = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k, _VALUE_TYPES.get(cfg.in_)
     _call(fn, dev, stream, ctypes.byref(cfg),
-          _addr(fn, "group_offsets", group_offsets, torch.int32, G + 1, dev), _addr(fn, "dy", dy, vt, R * n, dev),
-          _addr(fn, "w", w, vt, G * n * k, dev), _addr(fn, "da", da, _VALUE_TYPES.get(cfg.out), R * k, dev),
+          _addr(fn, "group_offsets", group_offsets, torch.int32, G + 1, dev), _addr(fn, "dy", dy, vt, R * n, dev, n),
+          _addr(fn, "w", w, vt, G * n * k, dev, k), _addr(fn, "da", da, _VALUE_TYPES.get(cfg.out), R * k, dev, k),
           *_workspace(fn, ws, dev))
 
 
@@ -416,8 +431,8 @@ def moe_grouped_gemm_wgrad(cfg: MoeProductConfig, group_offsets, dy, a, dw, ws, 
     dev = _device_of(dw, dy, a, group_offsets, ws)
     G, R, n, k, vt = cfg.n_groups, cfg.n_rows, cfg.n, cfg.k, _VALUE_TYPES.get(cfg.in_)
     _call(fn, dev, stream, ctypes.byref(cfg),
-          _addr(fn, "group_offsets", group_offsets, torch.int32, G + 1, dev), _addr(fn, "dy", dy, vt, R * n, dev),
-          _addr(fn, "a", a, vt, R * k, dev), _addr(fn, "dw", dw, _VALUE_TYPES.get(cfg.out), G * n * k, dev),
+          _addr(fn, "group_offsets", group_offsets, torch.int32, G + 1, dev), _addr(fn, "dy", dy, vt, R * n, dev, n),
+          _addr(fn, "a", a, vt, R * k, dev, k), _addr(fn, "dw", dw, _VALUE_TYPES.get(cfg.out), G * n * k, dev, k),
           *_workspace(fn, ws, dev))
 
 

@@ -4,6 +4,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 from sparse_expert_moe_b200 import moe
 
@@ -67,3 +68,41 @@ def test_scales_and_offsets_have_their_elements_alignment(lib):
     assert gemm(f8, sa=FAKE + 2, sw=FAKE) == 1 and gemm(f8, sa=FAKE, sw=FAKE + 1) == 1
     for fn in (lib.moe_grouped_gemm_dgrad, lib.moe_grouped_gemm_wgrad):
         assert fn(ctypes.byref(c), FAKE + 2, FAKE, FAKE, FAKE, FAKE, size, None) == 1
+
+
+def test_matrices_of_products_are_told_from_their_transposes(lib):
+    """A contiguous [G, k, n] has the elements of a [G, n, k] and is refused; flat tensors, rows split
+    into more dimensions and groups joined with rows are the same memory and pass (to the check of the
+    device, the last one, which these tensors on the host fail)."""
+    G, R, n, k = 4, 10, 256, 128
+    c, ws = moe.make_product_config(G, R, n, k), torch.zeros(16, dtype=torch.uint8)
+    f8 = moe.make_product_config(G, R, n, 256, dtype="e4m3_fs")
+
+    def t(*shape, dtype=torch.bfloat16):
+        return torch.zeros(*shape, dtype=dtype)
+
+    def calls(w):
+        yield lambda: moe.moe_grouped_gemm(c, FAKE, FAKE, None, w, None, FAKE, ws, stream=0)
+        yield lambda: moe.moe_grouped_gemm_dgrad(c, FAKE, FAKE, w, FAKE, ws, stream=0)
+        yield lambda: moe.moe_grouped_gemm_wgrad(c, FAKE, FAKE, FAKE, w, ws, stream=0)
+    for shape in ((G, k, n), (k, G * n), (G * k, n), (k, G, n)):
+        for call in calls(t(*shape)):
+            with pytest.raises(ValueError, match="rows of 128 elements"):
+                call()
+    for shape in ((G, n, k), (G * n, k), (G * n * k,), (G, n, 2, k // 2), (G, 2, n // 2, k), (G, n, k, 1)):
+        for call in calls(t(*shape)):
+            with pytest.raises(ValueError, match="not on the CUDA device"):
+                call()
+    for bad in (dict(a=t(k, R)), dict(y=t(n, R))):
+        a = dict(dict(a=FAKE, y=FAKE), **bad)
+        with pytest.raises(ValueError, match="rows of"):
+            moe.moe_grouped_gemm(c, FAKE, a["a"], None, FAKE, None, a["y"], ws, stream=0)
+    f32 = torch.float32
+    for bad in (dict(sa=t(2, R, dtype=f32)), dict(sw=t(2, G, 2, dtype=f32).view(2, G * 2))):
+        s = dict(dict(sa=FAKE, sw=FAKE), **bad)
+        with pytest.raises(ValueError, match="rows of 2 elements"):
+            moe.moe_grouped_gemm(f8, FAKE, FAKE, s["sa"], FAKE, s["sw"], FAKE, ws, stream=0)
+    one = moe.make_product_config(1, R, 128, 128, dtype="e4m3_fs")          # rows of one scale
+    for shape in ((R, 1), (1, R), (R,)):
+        with pytest.raises(ValueError, match="not on the CUDA device"):
+            moe.moe_grouped_gemm(one, FAKE, FAKE, t(*shape, dtype=f32), FAKE, FAKE, FAKE, ws, stream=0)
