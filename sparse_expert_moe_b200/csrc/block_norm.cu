@@ -134,6 +134,10 @@ __device__ __forceinline__ void rows_wait() {   // all but the newest kStages - 
 }
 __device__ __forceinline__ void rows_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
+// Threads of a CTA whose rows are staged: with one CTA per SM they have 128 registers each, which
+// hold two vectors per thread and array without spills (100 of them are used).
+constexpr int kRowThreads = 512;
+
 // One array's vectors of a thread in one stage: 16 or 32 bytes each, thread-interleaved, kPitch
 // threads apart (a constant, so that the places are immediate offsets).
 template <bool F32, int kPitch>
@@ -169,12 +173,12 @@ __device__ __forceinline__ Vec8 row8(const uint4* st, int slot, const void* base
 // kAll (staged): a branch with its norm, no full gate, both outputs and no vectors past the row's
 // end -- what a block normally has -- without the tests for it per vector.
 template <bool RES32, bool ACT32, int VPT, int kStages, bool kAll = false>
-__global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : (VPT == 2 ? 448 : 512), 1)
+__global__ void __launch_bounds__(kStages == 0 && VPT <= 2 ? 1024 : kRowThreads, 1)
     block_norm_kernel(const NormArgs p) {
   __shared__ float part[2][64];
   extern __shared__ uint4 ring[];
   constexpr bool kStaged = kStages > 0;
-  constexpr int kRing = kStaged ? kStages : 1, kPitch = kStaged ? (VPT == 2 ? 448 : 512) : 0;
+  constexpr int kRing = kStaged ? kStages : 1, kPitch = kStaged ? kRowThreads : 0;
   constexpr int kAtY = VPT * (RES32 ? 2 : 1), kAtGate = kAtY + VPT * (ACT32 ? 2 : 1);
   const int row = threadIdx.x / p.tpr, i0 = threadIdx.x - row * p.tpr;
   const int step = gridDim.x * p.rows;
@@ -387,10 +391,10 @@ struct NormGradArgs {
 // with the sum of the partials, 5.2 TB/s, 0.80 of the measured copy bandwidth; bound by
 // instructions (about 45 per element) and the shared-memory reads of the three passes.
 template <bool RES32, bool ACT32, int VPT, int kStages, bool kAll = false>
-__global__ void __launch_bounds__(512) block_norm_backward_kernel(const NormGradArgs p) {
+__global__ void __launch_bounds__(kRowThreads) block_norm_backward_kernel(const NormGradArgs p) {
   constexpr bool kSmem = VPT > 2, kStaged = kStages > 0;
   static_assert(!(kSmem && kStaged), "shared memory holds the column sums or the stages");
-  constexpr int kRing = kStaged ? kStages : 1, kPitch = kStaged ? 512 : 0;
+  constexpr int kRing = kStaged ? kStages : 1, kPitch = kStaged ? kRowThreads : 0;
   constexpr int kR = RES32 ? 2 : 1, kY = ACT32 ? 2 : 1;
   __shared__ float part[2][32 * 5];
   extern __shared__ uint4 ring[];              // kSmem: fp32 column sums [2][d]
@@ -694,7 +698,7 @@ BackwardShape backward_shape(int d) {
   BackwardShape s;
   s.vpt = nvec <= 32 ? 1 : (nvec <= 1024 ? 2 : 4);
   s.tpr = ((nvec + s.vpt - 1) / s.vpt + 31) / 32 * 32;
-  s.rows = 512 / s.tpr;
+  s.rows = kRowThreads / s.tpr;
   return s;
 }
 
@@ -733,16 +737,17 @@ cudaError_t launch_forward_typed(const NormArgs& a, cudaStream_t s) {
     // staged: one CTA per SM with as many rows as its threads hold vectors for, kStages - 1 turns
     // in flight, if every CTA gets at least that many.  (Two CTAs per SM leave 72 registers per
     // thread, which spill: 94 us against 83 at T = 8192, d = 7168 without a gate.)
-    constexpr int kStages = VPT == 2 ? 4 : 3, kPitch = VPT == 2 ? 448 : 512;
-    const size_t smem = static_cast<size_t>(kStages) * VPT * kPitch * 16 *
-                        ((RES32 ? 2 : 1) + ((a.y != nullptr) + (a.gate_kind == MOE_GATE_FULL)) * (ACT32 ? 2 : 1));
+    constexpr int kStages = VPT == 2 ? 4 : 3, kR = RES32 ? 2 : 1, kY = ACT32 ? 2 : 1;
+    constexpr size_t kUnit = static_cast<size_t>(kStages) * VPT * kRowThreads * 16;
+    const size_t smem = kUnit * (kR + ((a.y != nullptr) + (a.gate_kind == MOE_GATE_FULL)) * kY);
     NormArgs q = a;
-    q.rows = kPitch / a.tpr;                     // fill the CTA
+    q.rows = kRowThreads / a.tpr;                // fill the CTA
     const int threads = q.tpr * q.rows;
     if (smem <= kSmemPerSm && q.rows >= 1 && a.T >= static_cast<int64_t>(kStages) * kSms * q.rows) {
-      const bool all = a.y && a.w_post && a.w_pre && a.r_out && a.gate_kind != MOE_GATE_FULL && a.nvec == VPT * a.tpr;
-      auto kernel = all ? block_norm_kernel<RES32, ACT32, VPT, kStages, true>
-                        : block_norm_kernel<RES32, ACT32, VPT, kStages, false>;
+      auto kernel = block_norm_kernel<RES32, ACT32, VPT, kStages, false>;
+      if constexpr (kUnit * (kR + kY) <= kSmemPerSm)              // (a branch without a full gate fits)
+        if (a.y && a.w_post && a.w_pre && a.r_out && a.gate_kind != MOE_GATE_FULL && a.nvec == VPT * a.tpr)
+          kernel = block_norm_kernel<RES32, ACT32, VPT, kStages, true>;
       const cudaError_t e =
           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return e;
@@ -764,10 +769,10 @@ cudaError_t launch_forward(const NormArgs& a, bool res32, bool act32, cudaStream
 template <bool RES32, bool ACT32, int VPT>
 cudaError_t launch_backward_typed(const NormGradArgs& a, unsigned grid, cudaStream_t s) {
   const int threads = a.tpr * a.rows;
-  if constexpr (VPT <= 2) {
-    constexpr int kStages = 3;
-    const size_t smem = static_cast<size_t>(kStages) * VPT * 512 * 16 *
-                        (2 * (RES32 ? 2 : 1) + (2 + (a.gate_kind == MOE_GATE_FULL)) * (ACT32 ? 2 : 1));
+  constexpr int kStages = 3, kR = RES32 ? 2 : 1, kY = ACT32 ? 2 : 1;
+  constexpr size_t kUnit = static_cast<size_t>(kStages) * VPT * kRowThreads * 16;
+  if constexpr (VPT <= 2 && kUnit * (2 * kR + 2 * kY) <= kSmemPerSm) {            // (without a full gate it fits)
+    const size_t smem = kUnit * (2 * kR + (2 + (a.gate_kind == MOE_GATE_FULL)) * kY);
     if (smem <= kSmemPerSm && a.T > 2 * static_cast<int64_t>(grid) * a.rows) {
       const bool all = a.y && a.w_post && a.w_pre && a.dr_out && a.gate_kind != MOE_GATE_FULL && a.nvec == VPT * a.tpr;
       auto kernel = all ? block_norm_backward_kernel<RES32, ACT32, VPT, kStages, true>
@@ -834,9 +839,12 @@ moe_status moe_block_norm(const moe_norm_config* cfg, const void* r, const void*
   a.res_scale = cfg->res_scale;
   a.branch_scale = cfg->branch_scale;
   a.w_offset = cfg->w_offset;
-  // few tokens: as many threads per row as it has vectors, for the shortest chain; many: four
-  // vectors per thread, which keeps more loads in flight per thread and more CTAs on an SM
-  const int vpt = a.nvec > 2048 ? 4 : (cfg->T <= 296 ? (a.nvec <= 1024 ? 1 : 2) : (a.nvec <= 64 ? 1 : (a.nvec <= 896 ? 2 : 4)));
+  // few tokens (two rows per SM): as many threads per row as it has vectors, for the shortest chain
+  // (d = 4096: 128 rows 3.0 us so, 3.9 with two vectors per thread; 1000 rows 10.5 against 9.6);
+  // many: two vectors per thread, rows staged (d = 8192, 8192 rows, fp32 residual: 156 us, 232 with
+  // four vectors, whose stages do not fit), and four where kRowThreads threads need them
+  const int vpt = cfg->T <= 2 * kSms ? (a.nvec <= 1024 ? 1 : 2)
+                                     : (a.nvec <= 64 ? 1 : (a.nvec <= 2 * kRowThreads ? 2 : 4));
   a.tpr = ((a.nvec + vpt - 1) / vpt + 31) / 32 * 32;
   a.rows = a.tpr >= 128 ? 1 : 128 / a.tpr;
   const bool res32 = cfg->res == MOE_F32, act32 = cfg->act == MOE_F32;
