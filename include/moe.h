@@ -326,7 +326,8 @@ MOE_API moe_status moe_norm_workspace_size(const moe_norm_config *cfg, size_t *b
  *   r_out = res_scale * r + branch_scale * gate * u
  *   h     = norm(r_out; w_pre)
  *   norm(x; w) = x / sqrt(mean(x^2) + eps) * (w + w_offset)   per token
- * in fp32 registers, each output rounded once (h from the unrounded r_out).
+ * in fp32 registers, each output rounded once (h from the unrounded r_out).  The sum of a row's
+ * squares is fp32 as well: it has to stay below 3.4e38.
  *   y      NULL: no branch (r_out = res_scale * r; gate and w_post NULL, gate kind NONE)
  *   w_pre  NULL: no second norm (h NULL)
  *   r_out  NULL: not stored
@@ -365,6 +366,10 @@ MOE_API moe_status moe_block_norm_backward(const moe_norm_config *cfg, const voi
  *        moe_grouped_gemm only)
  *   out  MOE_BF16 or MOE_F32
  * 1 <= n_groups <= 1024; n, k <= 65536; n_rows <= 2^24.
+ * n_rows may be more than the groups hold, but it is also what the kernel is chosen by (at most 8
+ * rows per group on average, or 32 in all, 64 in e4m3: tiles of few rows): a call for a few rows
+ * at the head of a large buffer is faster with their number, or a bound near it, as n_rows.
+ * Products of bf16 are summed 512 at a time on the tensor cores, and those sums in fp32.
  * Calls that share a workspace must not overlap on the GPU.  Tiles that several CTAs sum up
  * are joined in a fixed order: reruns are bit-identical.  After MOE_ERR_TIMEOUT the header must
  * be reset (moe_reset_device_status) before the workspace is used again. */

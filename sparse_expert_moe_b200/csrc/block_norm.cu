@@ -163,12 +163,12 @@ __device__ __forceinline__ Vec8 row8(const uint4* st, int slot, const void* base
 // into registers: c = branch_scale (w_post + o) (channel gate), and w_pre + o.
 //
 // Bound by HBM where rows are many.  Measured at T = 8192, d = 7168, bf16, post-norm, token gate
-// and pre-norm (470 MB): 73 us, 6.4 TB/s, 0.98 of the measured copy bandwidth.  On the way there:
-// one row per CTA, weights fetched per row 172 us (a row's loads and its two sums took turns);
-// rows staged 134 us (50 instructions per element, issued 57% of the time); packed arithmetic, the
-// weights in registers, one barrier per row 96 us; no tests per vector, one CTA per SM without
-// spills and the token gate's bits fetched a row ahead 74 us; launches that overlap 73 us (the
-// backward 70 -> 67 us, one token 4.0 -> 3.8 us).
+// and pre-norm (470 MB): 72 us alone, 78 in a run of cases back to back, 6.1-6.5 TB/s, 0.93-1.0 of the
+// measured copy bandwidth; 21 instructions per element, issued in 48% of the cycles.  On the way there:
+// one row per CTA, weights fetched per row 172 us (a row's loads and its two sums took turns); rows
+// staged 134 us; packed arithmetic, the weights in registers, one barrier per row 96 us; no tests per
+// vector, one CTA per SM without spills and the token gate's bits fetched a row ahead 74 us.  Launches
+// that overlap: one token 4.0 -> 3.8 us.
 //
 // kAll (staged): a branch with its norm, no full gate, both outputs and no vectors past the row's
 // end -- what a block normally has -- without the tests for it per vector.
@@ -387,9 +387,10 @@ struct NormGradArgs {
 // keeps those of its own vectors in registers (VPT <= 2) or in its own places of shared memory,
 // and writes them at the end as one partial per row slot.
 //
-// Measured at T = 4095, d = 7168, bf16, both norms, channel gate, all gradients (352 MB): 67 us
-// with the sum of the partials, 5.2 TB/s, 0.80 of the measured copy bandwidth; bound by
-// instructions (about 45 per element) and the shared-memory reads of the three passes.
+// Measured at T = 4095, d = 7168, bf16, both norms, channel gate, all gradients (352 MB): 72 us
+// with the sum of the partials, 4.9 TB/s, 0.75 of the measured copy bandwidth; bound by
+// instructions (41 per element with a token gate, issued in 50% of the cycles) and the shared-memory
+// reads of the three passes.
 template <bool RES32, bool ACT32, int VPT, int kStages, bool kAll = false>
 __global__ void __launch_bounds__(kRowThreads) block_norm_backward_kernel(const NormGradArgs p) {
   constexpr bool kSmem = VPT > 2, kStaged = kStages > 0;

@@ -22,8 +22,8 @@
 // up under its last CTAs, and launch_wait() stands before the first access to global memory (one
 // bf16 token of 128 x 128: 5.2 -> 4.3 us; one token in eight of 64 groups, 4096 x 7168: 80.3 -> 77.7 us).
 //
-// Warp roles: 0 TMA producer, 1 MMA issuer (and TMEM owner), 2 scales (stream kernel, e4m3) or
-// the zeroing of rows behind a group's last (TN), then the epilogue warps.  Producer and issuer
+// Warp roles: 0 TMA producer, 1 MMA issuer (and TMEM owner), 2 scales (e4m3; in the fold
+// kernel 2 and 3) or the zeroing of rows behind a group's last (TN), then the epilogue warps.  Producer and issuer
 // keep the whole warp in their loops and let one elected lane issue: TMA and MMA instructions take
 // their operands from uniform registers, and a branch on the lane number costs a transfer for
 // each of them (pair kernel, TN, 8192 x 4096 x 7168: 1274 TFLOP/s so, 1460 uniform).
@@ -490,7 +490,7 @@ __device__ __forceinline__ bool scales_overflow(float a, float b) {
 // Measured: 64 groups, n = 7168, k = 2048, 512 rows: 6.43 TB/s (0.98 of a copy); one token's 8
 // groups of n = 4096, k = 7168 78 us (6.0 TB/s: about 6 us are the start, first loads and the
 // join of the cut tiles).  One e4m3 token, n = 7168, k = 2048: 9.6 us, latency: the start of
-// the CTA and its first loads, three K blocks, the join of the parts.
+// the CTA and its first loads, four K blocks, the join of the parts.
 template <bool F8, int OP>
 struct StreamCfg {
   static constexpr int kMB = 2;                                   // 128-row weight blocks per tile
@@ -812,8 +812,8 @@ __global__ void __launch_bounds__(224, 1) stream_kernel(const __grid_constant__ 
 // store a finished tile, under the MMAs of the next.
 //
 // Measured: one group of 8192 rows, n = 4096, k = 7168: 325 us for NT (1480 TFLOP/s), 336 for NN,
-// 350-440 for TN; one K block takes 513 cycles, of which the MMAs need 512, and the 1000 W power limit
-// holds the clock near 1.2 GHz in a loop of them.  fp32 output: 335-357, 370-390 and 430-470.  One
+// 350-440 for TN.  Alone on a cool GPU the tensor pipe is busy in 93% of the cycles (TN with fp32
+// output: 77%); in a loop the 1000 W power limit holds the clock near 1.2 GHz.  fp32 output: 335-357, 370-390 and 430-470.  One
 // accumulator for the whole sum, stored as bf16, took 310, 317 and 335-400.  TN of 32 groups x 256
 // rows, n = 7168, k = 2048, fp32: 460 us; a tile has four K blocks there for 256 KB of sums, so the
 // stores bound it.
@@ -1209,13 +1209,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<OP>::kThread
 // One commit per K block says both that its products are in TMEM and that its stage is free.  The
 // scales come through shared memory, fetched by the two warps that are free otherwise.
 //
-// Measured at that size: 243 us, 1980 TFLOP/s, 0.75 of cuBLASLt's plain e4m3 rate (sustained).
-// A K block takes about 1040 cycles, of which the MMAs need 512 at full rate.  Loads alone, with
-// neither MMAs nor folds, take 146 us there, loads and MMAs 200 us, loads and folds 200 us: what
-// is left is that the two overlap in part only, with the two buffers that TMEM has room for.  On
-// the way: two 128-column MMAs and four buffers 312 us (the token operand is read twice), sixteen
-// epilogue warps 365 us (twice the waits), scales loaded by the epilogue threads two K blocks ahead
-// 254 us, 32-column loads two at a time 318 us (registers spill).  CTA pairs with 256 tokens:
+// Measured at that size: 243 us on a cool GPU (1980 TFLOP/s, 0.75 of cuBLASLt's plain e4m3 rate,
+// sustained), 290 us in a run of cases back to back.  A K block takes about 1020 cycles, of which the
+// MMAs need 512 at full rate (tensor pipe busy in 51% of the cycles).  Loads alone, with neither MMAs
+// nor folds, take 146 us there, loads and MMAs 200 us, loads and folds 200 us: what is left is that
+// the two overlap in part only, with the two buffers that TMEM has room for.  On the way (cool): two
+// 128-column MMAs and four buffers 312 us (the token operand is read twice), sixteen epilogue warps
+// 365 us (twice the waits), scales loaded by the epilogue threads two K blocks ahead 254 us,
+// 32-column loads two at a time 318 us (registers spill).  CTA pairs with 256 tokens:
 // 245 us, and 450 us where 64 groups have 16 rows each (293 us here); pairs on 128-column tiles
 // with four buffers 307 us.
 struct FoldCfg {
@@ -1574,7 +1575,7 @@ moe_status launch_product(const ProductArgs& a, bool f32, bool stream_tiles, cud
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// Groups of few rows go to the stream kernel (only the average is known on the host): at most 32
+// Groups of few rows go to the stream kernel (the host knows the rows' capacity and the groups): at most 32
 // rows in all (e4m3: 64, two tiles' rows), or at most eight per group on average, where few groups
 // hold more than a tile.  Measured with 64 groups, n = 7168, k = 2048: 8 rows on average 6.43 TB/s, 16
 // rows 5.7 (groups above 32 rows read their weights twice), against 6.3 with 32 rows in the pair
